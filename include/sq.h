@@ -68,7 +68,9 @@ typedef enum {
                              tensor was caught and that access skipped (from sq_sync_status) */
 } sq_status;
 
-typedef enum { SQ_F32 = 0, SQ_BF16 = 1 } sq_dtype;
+/* SQ_F32 and SQ_BF16 are the activation, weight and output types; the other
+ * three are taken only where an argument's description names them. */
+typedef enum { SQ_F32 = 0, SQ_BF16 = 1, SQ_I8 = 2, SQ_I32 = 3, SQ_I64 = 4 } sq_dtype;
 
 /* Activation quantization granularity ([review] §2.5, §2.6 Fig. 3, §6.3):
  * per-tensor with a static step fixed at calibration (SmoothQuant-O3),
@@ -254,6 +256,150 @@ sq_status sq_rms_smooth_quant_act(const void* x, sq_dtype xt, int64_t T,
                                   sq_act_gran gran, float* act_scale,
                                   int8_t* xq, int64_t* n_clipped,
                                   sq_stream stream);
+
+/*
+ * sq_add_rms_smooth_quant_act -- the residual stream's addition in front of
+ * the RMSNorm quantizer, in one pass (no counterpart on the pages: the
+ * pre-norm residual block the RMSNorm fold is used in):
+ *
+ *   h[t,k] = x[t,k] + residual[t,k]   (one fp32 addition, rounded to type xt)
+ *
+ * then exactly sq_rms_smooth_quant_act on the stored h: the same codes,
+ * steps and clip counts bit for bit, at every granularity.
+ *
+ *   x, residual [T,K] type xt; h [T,K] type xt out (the new residual stream;
+ *   it may be x or residual itself, any other overlap is not allowed).
+ * All other arguments and the errors as sq_rms_smooth_quant_act.
+ */
+sq_status sq_add_rms_smooth_quant_act(const void* x, const void* residual,
+                                      sq_dtype xt, int64_t T, int64_t K,
+                                      const float* gamma_s, float eps,
+                                      sq_act_gran gran, void* h,
+                                      float* act_scale, int8_t* xq,
+                                      int64_t* n_clipped, sq_stream stream);
+
+/*
+ * Routed experts (no counterpart on the pages: the layer's linears as
+ * experts chosen per token).  A router gives every token t its top_k
+ * experts; assignment (t, c) is the token's c-th.  sq_moe_sort orders the
+ * assignments by expert, sq_moe_gather copies the tokens' codes into that
+ * order, sq_gemm_w8a8_grouped multiplies every expert's rows with its
+ * weights, sq_moe_combine brings the rows back to their tokens, and
+ * sq_moe_combine_grad is its gradient.
+ *
+ *   offsets [E+1] int32: expert e's rows are offsets[e] .. offsets[e+1] - 1.
+ *   pos [T, top_k] int32: the sorted row of each assignment, or -1.
+ * Both stay on the device; no call reads them on the host.  T * top_k and the
+ * row counts R must be below 2^31, E in [1, 1024], top_k >= 1, a row's width
+ * (K or N) in [1, 2^20].  Any other value is SQ_ERR_SHAPE.
+ */
+
+/*
+ * sq_moe_sort -- assignments sorted by expert, stable (an expert's rows are
+ * in the order of token, then choice):
+ *
+ *   offsets[e] = #{(t, c) : expert_ids[t,c] in [0, e)}
+ *   pos[t,c]   = offsets[expert_ids[t,c]] + the earlier assignments to it
+ *
+ *   expert_ids [T, top_k] of type it (SQ_I32 or SQ_I64).  An id outside
+ *   [0, E) (padding, a dropped assignment) goes nowhere: pos = -1.  A token
+ *   may name an expert twice.
+ *   workspace: at least sq_moe_sort_workspace_bytes(T, top_k, E) bytes (0 for
+ *   up to 2048 assignments; it needs no initialization; concurrent calls must
+ *   not share one).
+ * T = 0 sets every offset to 0.
+ */
+size_t sq_moe_sort_workspace_bytes(int64_t T, int64_t top_k, int64_t E);
+sq_status sq_moe_sort(const void* expert_ids, sq_dtype it, int64_t T,
+                      int64_t top_k, int64_t E, int32_t* offsets, int32_t* pos,
+                      void* workspace, size_t workspace_bytes,
+                      sq_stream stream);
+
+/*
+ * sq_moe_gather -- each token's row copied to its sorted rows:
+ *
+ *   xs[pos[t,c], :] = x[t, :],   scale_out[pos[t,c]] = scale[t]
+ *
+ *   x [T,K] and xs [R,K] of type xt (SQ_I8, SQ_BF16 or SQ_F32).
+ *   scale [T] / scale_out [R] fp32: the rows' steps, both or neither.
+ *   Assignments whose pos is outside [0, R) are skipped; rows of xs that no
+ *   assignment points to keep what they held.  Two assignments must not point
+ *   to the same row.
+ * Its gradient (of a floating xs) is sq_moe_combine of the rows' gradients
+ * without weights.
+ */
+sq_status sq_moe_gather(const void* x, sq_dtype xt, int64_t T, int64_t K,
+                        const float* scale, const int32_t* pos, int64_t top_k,
+                        int64_t R, void* xs, float* scale_out,
+                        sq_stream stream);
+
+/*
+ * sq_moe_combine -- the experts' rows back to their tokens:
+ *
+ *   y[t,n] = residual[t,n] + sum_c w[t,c] * z[pos[t,c], n]
+ *
+ *   z [R,N], residual [T,N] (or NULL: 0) and y [T,N] of type t (SQ_F32 or
+ *   SQ_BF16); w [T, top_k] fp32, or NULL: 1.  In fp32 from the residual, c
+ *   increasing, one fused multiply-add per term (an addition without w), and
+ *   rounded once.  Assignments whose pos is outside [0, R) add nothing (their
+ *   rows are not read), so a token of none gives residual[t] or 0.  y may be
+ *   the residual itself; z must not overlap y.
+ */
+sq_status sq_moe_combine(const void* z, sq_dtype t, int64_t R, int64_t N,
+                         const int32_t* pos, const float* w, int64_t T,
+                         int64_t top_k, const void* residual, void* y,
+                         sq_stream stream);
+
+/*
+ * sq_moe_combine_grad -- the gradients of sq_moe_combine for the output
+ * gradient dy [T,N]:
+ *
+ *   dz[pos[t,c], n] = w[t,c] * dy[t,n]
+ *   dw[t,c]         = sum_n dy[t,n] * z[pos[t,c], n]
+ *
+ *   dz [R,N] (type t, as dy and z) or NULL, dw [T, top_k] fp32 or NULL; z is
+ *   read only for dw (else it may be NULL); w NULL: 1.  dw is summed in fp32
+ *   in one fixed order.  Assignments whose pos is outside [0, R) get dw = 0;
+ *   rows of dz that no assignment points to keep what they held.  The
+ *   residual's gradient is dy.  The arrays must not overlap.
+ */
+sq_status sq_moe_combine_grad(const void* dy, sq_dtype t, int64_t T, int64_t N,
+                              const int32_t* pos, const float* w,
+                              int64_t top_k, const void* z, int64_t R,
+                              void* dz, float* dw, sq_stream stream);
+
+/*
+ * sq_gemm_w8a8_grouped -- sq_gemm_w8a8_bias with one weight matrix per group
+ * of rows, the groups given on the device:
+ *
+ *   acc[r,n] = sum_k xq[r,k] * wq[e,n,k]      for offsets[e] <= r < offsets[e+1]
+ *   y[r,n]   = (float)acc[r,n] * (as_r * w_scale[e,n]) (+ bias[e,n])
+ *   as_r     = act_scale[r] if act_per_token else act_scale[0]
+ *
+ * bit for bit what sq_gemm_w8a8_bias gives on each group.
+ *
+ *   xq [R,K] int8; wq [E,N,K] int8; offsets [E+1] int32 (sq_moe_sort's);
+ *   w_scale [E,N] and bias [E,N] (or NULL) fp32; y [R,N] of type yt (SQ_F32 or
+ *   SQ_BF16); acc_out NULL or [R,N] int32.
+ *   Rows before offsets[0] and from offsets[E] on keep what they held.
+ *   Offsets must be non-decreasing in [0, R]; values that are not are clamped
+ *   (rows may then go to another expert, but nothing outside the arrays is
+ *   touched).  An expert may have no rows; its weights are then not read.
+ *   workspace: at least sq_gemm_w8a8_grouped_workspace_bytes(R,N,K,E) bytes,
+ *   16-byte aligned (may be NULL when that is 0); it needs no initialization
+ *   and concurrent calls must not share one.
+ * K as everywhere; errors as sq_gemm_w8a8; (R / 128 + E) times the 128-column
+ * tiles of N must stay below 2^31.
+ */
+size_t sq_gemm_w8a8_grouped_workspace_bytes(int64_t R, int64_t N, int64_t K,
+                                            int64_t E);
+sq_status sq_gemm_w8a8_grouped(const int8_t* xq, const int8_t* wq,
+                               const int32_t* offsets, int64_t R, int64_t N,
+                               int64_t K, int64_t E, const float* act_scale,
+                               int act_per_token, const float* w_scale,
+                               const float* bias, void* y, sq_dtype yt,
+                               int32_t* acc_out, void* workspace,
+                               size_t workspace_bytes, sq_stream stream);
 
 /*
  * sq_gemm_workspace_bytes -- device scratch sq_gemm_w8a8 needs for this

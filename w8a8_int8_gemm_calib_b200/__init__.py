@@ -20,7 +20,7 @@ import torch
 
 from . import _lib
 from ._lib import (SQ_ACT_PER_TENSOR_DYNAMIC, SQ_ACT_PER_TENSOR_STATIC, SQ_ACT_PER_TOKEN_DYNAMIC, SQ_BF16,
-                   SQ_F32, SQError, check, lib)
+                   SQ_F32, SQ_I8, SQ_I32, SQ_I64, SQError, check, lib)
 
 __all__ = [
     "sq_calib_absmax", "sq_smooth_scales", "sq_fuse_weights_q8",
@@ -30,6 +30,9 @@ __all__ = [
     "sq_alpha_sweep_workspace_bytes", "sq_alpha_sweep", "sq_bmm_w8a8",
     "sq_weight_colmax", "sq_smooth_scales_peaks", "sq_probe_mma_i8", "sq_probe_mma_i8_pair",
     "sq_debug_bounds_enabled", "sq_selftest_bounds_check",
+    "sq_add_rms_smooth_quant_act", "sq_moe_sort_workspace_bytes", "sq_moe_sort",
+    "sq_moe_gather", "sq_moe_combine", "sq_moe_combine_grad",
+    "sq_gemm_w8a8_grouped_workspace_bytes", "sq_gemm_w8a8_grouped",
 ]
 
 
@@ -140,6 +143,122 @@ def sq_rms_smooth_quant_act(x, xq, act_scale, gamma_s, eps=1e-5, per_token=True,
     return xq, act_scale
 
 
+_ROW_TYPES = {torch.float32: SQ_F32, torch.bfloat16: SQ_BF16, torch.int8: SQ_I8}
+_ID_TYPES = {torch.int32: SQ_I32, torch.int64: SQ_I64}
+
+
+def _arg(t, what, dtype, numel):
+    """Pointer of a contiguous tensor of this type and size on the current
+    device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{what}: expected {numel} elements, got {t.numel()}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: not on the current CUDA device")
+    return _ptr(t)
+
+
+def _scratch(workspace, need, what):
+    """(pointer, bytes) of a Workspace or a uint8 tensor of at least `need` bytes."""
+    if not need:
+        return None, 0
+    if workspace is None:
+        raise ValueError(f"{what} needs a workspace of {need} bytes")
+    ws = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def sq_add_rms_smooth_quant_act(x, residual, h, xq, act_scale, gamma_s, eps=1e-5, per_token=True,
+                                n_clipped=None, stream=None, per_tensor_dynamic=False):
+    """h = x + residual, then sq_rms_smooth_quant_act of the stored h, in one
+    pass -> h, xq (and act_scale).  h may be x or residual itself."""
+    T, K = x.shape
+    dt = x.dtype
+    if per_tensor_dynamic:
+        gran = SQ_ACT_PER_TENSOR_DYNAMIC
+    else:
+        gran = SQ_ACT_PER_TOKEN_DYNAMIC if per_token else SQ_ACT_PER_TENSOR_STATIC
+    steps = T if gran == SQ_ACT_PER_TOKEN_DYNAMIC else 1
+    check(lib.sq_add_rms_smooth_quant_act(
+        _arg(x, "x", dt, T * K), _arg(residual, "residual", dt, T * K), _dt(x), T, K,
+        _arg(gamma_s, "gamma_s", torch.float32, K), eps, gran, _arg(h, "h", dt, T * K),
+        _arg(act_scale, "act_scale", torch.float32, steps), _arg(xq, "xq", torch.int8, T * K),
+        _arg(n_clipped, "n_clipped", torch.int64, 1), _stream(stream)),
+        "sq_add_rms_smooth_quant_act")
+    return h, xq, act_scale
+
+
+def sq_moe_sort_workspace_bytes(T, top_k, E) -> int:
+    return int(lib.sq_moe_sort_workspace_bytes(T, top_k, E))
+
+
+def sq_moe_sort(expert_ids, num_experts, offsets, pos, workspace=None, stream=None):
+    """Assignments sorted by expert: expert_ids [T, top_k] int32 or int64 (an
+    id outside [0, E): none) -> offsets [E + 1], pos [T, top_k] int32."""
+    T, k = expert_ids.shape
+    if expert_ids.dtype not in _ID_TYPES:
+        raise TypeError(f"expert_ids: expected int32 or int64, got {expert_ids.dtype}")
+    ws, nbytes = _scratch(workspace, sq_moe_sort_workspace_bytes(T, k, num_experts), "sq_moe_sort")
+    check(lib.sq_moe_sort(_arg(expert_ids, "expert_ids", expert_ids.dtype, T * k),
+                          _ID_TYPES[expert_ids.dtype], T, k, num_experts,
+                          _arg(offsets, "offsets", torch.int32, num_experts + 1),
+                          _arg(pos, "pos", torch.int32, T * k), ws, nbytes, _stream(stream)),
+          "sq_moe_sort")
+    return offsets, pos
+
+
+def sq_moe_gather(x, pos, xs, scale=None, scale_s=None, stream=None):
+    """Each token's row (int8, bf16 or fp32), and its step, copied to its
+    sorted rows: xs[pos[t, c]] = x[t], scale_s[pos[t, c]] = scale[t]."""
+    T, K = x.shape
+    R, k = xs.shape[0], pos.shape[1]
+    if x.dtype not in _ROW_TYPES:
+        raise TypeError(f"x: expected int8, bfloat16 or float32, got {x.dtype}")
+    check(lib.sq_moe_gather(_arg(x, "x", x.dtype, T * K), _ROW_TYPES[x.dtype], T, K,
+                            _arg(scale, "scale", torch.float32, T),
+                            _arg(pos, "pos", torch.int32, T * k), k, R,
+                            _arg(xs, "xs", x.dtype, R * K),
+                            _arg(scale_s, "scale_s", torch.float32, R), _stream(stream)),
+          "sq_moe_gather")
+    return xs, scale_s
+
+
+def sq_moe_combine(z, pos, y, weights=None, residual=None, stream=None):
+    """y[t] = residual[t] + sum_c weights[t, c] * z[pos[t, c]] (weights None:
+    1; without weights and residual the gradient of sq_moe_gather).  y may be
+    the residual itself."""
+    R, N = z.shape
+    T, k = pos.shape
+    check(lib.sq_moe_combine(_arg(z, "z", z.dtype, R * N), _dt(z), R, N,
+                             _arg(pos, "pos", torch.int32, T * k),
+                             _arg(weights, "weights", torch.float32, T * k), T, k,
+                             _arg(residual, "residual", z.dtype, T * N),
+                             _arg(y, "y", z.dtype, T * N), _stream(stream)), "sq_moe_combine")
+    return y
+
+
+def sq_moe_combine_grad(dy, pos, z=None, weights=None, dz=None, dweights=None, stream=None):
+    """Gradients of sq_moe_combine: dz[pos[t, c]] = weights[t, c] * dy[t] and
+    dweights[t, c] = <dy[t], z[pos[t, c]]>, each where its output is given."""
+    T, N = dy.shape
+    k = pos.shape[1]
+    rows = dz if dz is not None else z
+    R = 0 if rows is None else rows.shape[0]
+    if dweights is not None and z is None:
+        raise ValueError("dweights needs z")
+    check(lib.sq_moe_combine_grad(_arg(dy, "dy", dy.dtype, T * N), _dt(dy), T, N,
+                                  _arg(pos, "pos", torch.int32, T * k),
+                                  _arg(weights, "weights", torch.float32, T * k), k,
+                                  _arg(z, "z", dy.dtype, R * N), R,
+                                  _arg(dz, "dz", dy.dtype, R * N),
+                                  _arg(dweights, "dweights", torch.float32, T * k),
+                                  _stream(stream)), "sq_moe_combine_grad")
+    return dz, dweights
+
+
 def sq_fold_into_producer(s, w_scale, bias=None, stream=None):
     """1/s folded into the producing linear: w_scale /= s, bias /= s (in place)."""
     K = s.numel()
@@ -229,6 +348,31 @@ def sq_gemm_w8a8(xq, wq, act_scale, w_scale, y, per_token=True, acc_out=None,
                                     int(per_token), _ptr(w_scale), _ptr(bias), _ptr(y), _dt(y),
                                     _ptr(acc_out), _ptr(ws), nbytes, _stream(stream)),
               "sq_gemm_w8a8_bias")
+    return y
+
+
+def sq_gemm_w8a8_grouped_workspace_bytes(R, N, K, E) -> int:
+    return int(lib.sq_gemm_w8a8_grouped_workspace_bytes(R, N, K, E))
+
+
+def sq_gemm_w8a8_grouped(xq, wq, offsets, act_scale, w_scale, y, per_token=True, bias=None,
+                         acc_out=None, workspace=None, stream=None):
+    """The experts' GEMM: rows offsets[e] .. offsets[e + 1] - 1 of xq [R, K]
+    with wq[e] of [E, N, K], dequantized by act_scale and w_scale [E, N] (+
+    bias [E, N]); y [R, N] fp32 or bf16."""
+    R, K = xq.shape
+    E, N, _ = wq.shape
+    ws, nbytes = _scratch(workspace, sq_gemm_w8a8_grouped_workspace_bytes(R, N, K, E),
+                          "sq_gemm_w8a8_grouped")
+    check(lib.sq_gemm_w8a8_grouped(_arg(xq, "xq", torch.int8, R * K),
+                                   _arg(wq, "wq", torch.int8, E * N * K),
+                                   _arg(offsets, "offsets", torch.int32, E + 1), R, N, K, E,
+                                   _arg(act_scale, "act_scale", torch.float32, R if per_token else 1),
+                                   int(per_token), _arg(w_scale, "w_scale", torch.float32, E * N),
+                                   _arg(bias, "bias", torch.float32, E * N),
+                                   _arg(y, "y", y.dtype, R * N), _dt(y),
+                                   _arg(acc_out, "acc_out", torch.int32, R * N), ws, nbytes,
+                                   _stream(stream)), "sq_gemm_w8a8_grouped")
     return y
 
 

@@ -29,6 +29,9 @@ SQ_ERR_BOUNDS = 9
 
 SQ_F32 = 0
 SQ_BF16 = 1
+SQ_I8 = 2
+SQ_I32 = 3
+SQ_I64 = 4
 SQ_ACT_PER_TENSOR_STATIC = 0
 SQ_ACT_PER_TOKEN_DYNAMIC = 1
 SQ_ACT_PER_TENSOR_DYNAMIC = 2
@@ -42,6 +45,9 @@ EXPORTS = [
     "sq_alpha_sweep_workspace_bytes", "sq_alpha_sweep", "sq_bmm_w8a8",
     "sq_weight_colmax", "sq_smooth_scales_peaks", "sq_probe_mma_i8", "sq_probe_mma_i8_pair",
     "sq_debug_bounds_enabled", "sq_selftest_bounds_check",
+    "sq_add_rms_smooth_quant_act", "sq_moe_sort_workspace_bytes", "sq_moe_sort",
+    "sq_moe_gather", "sq_moe_combine", "sq_moe_combine_grad",
+    "sq_gemm_w8a8_grouped_workspace_bytes", "sq_gemm_w8a8_grouped",
 ]
 
 
@@ -88,12 +94,24 @@ def _load() -> ctypes.CDLL:
     L.sq_debug_bounds_enabled.restype = i
     L.sq_selftest_bounds_check.argtypes = [p]
     L.sq_gemm_w8a8_noalloc.argtypes = [p, p, i64, i64, i64, p, i, p, p, i, p, p]
+    L.sq_add_rms_smooth_quant_act.argtypes = [p, p, i, i64, i64, p, f, i, p, p, p, p, p]
+    L.sq_moe_sort_workspace_bytes.argtypes = [i64, i64, i64]
+    L.sq_moe_sort_workspace_bytes.restype = sz
+    L.sq_moe_sort.argtypes = [p, i, i64, i64, i64, p, p, p, sz, p]
+    L.sq_moe_gather.argtypes = [p, i, i64, i64, p, p, i64, i64, p, p, p]
+    L.sq_moe_combine.argtypes = [p, i, i64, i64, p, p, i64, i64, p, p, p]
+    L.sq_moe_combine_grad.argtypes = [p, i, i64, i64, p, p, i64, p, i64, p, p, p]
+    L.sq_gemm_w8a8_grouped_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.sq_gemm_w8a8_grouped_workspace_bytes.restype = sz
+    L.sq_gemm_w8a8_grouped.argtypes = [p, p, p, i64, i64, i64, i64, p, i, p, p, p, i, p, p, sz, p]
     for fn in ("sq_calib_absmax", "sq_smooth_scales", "sq_fuse_weights_q8",
                "sq_ln_smooth_quant_act", "sq_gemm_w8a8", "sq_sync_status",
                "sq_selftest_bounded_wait", "sq_gemm_w8a8_noalloc", "sq_gemm_w8a8_bias",
                "sq_calib_absmax_rms", "sq_rms_smooth_quant_act", "sq_fold_into_producer",
                "sq_alpha_sweep", "sq_bmm_w8a8", "sq_weight_colmax", "sq_smooth_scales_peaks",
-               "sq_probe_mma_i8", "sq_probe_mma_i8_pair", "sq_selftest_bounds_check"):
+               "sq_probe_mma_i8", "sq_probe_mma_i8_pair", "sq_selftest_bounds_check",
+               "sq_add_rms_smooth_quant_act", "sq_moe_sort", "sq_moe_gather", "sq_moe_combine",
+               "sq_moe_combine_grad", "sq_gemm_w8a8_grouped"):
         getattr(L, fn).restype = st
     return L
 

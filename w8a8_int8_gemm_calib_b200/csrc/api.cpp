@@ -287,6 +287,217 @@ sq_status sq_rms_smooth_quant_act(const void* x, sq_dtype xt, int64_t T, int64_t
                     gran, act_scale, xq, n_clipped, stream);
 }
 
+sq_status sq_add_rms_smooth_quant_act(const void* x, const void* residual, sq_dtype xt, int64_t T,
+                                      int64_t K, const float* gamma_s, float eps,
+                                      sq_act_gran gran, void* h, float* act_scale, int8_t* xq,
+                                      int64_t* n_clipped, sq_stream stream) {
+  const char* fn = "sq_add_rms_smooth_quant_act";
+  g_last_error[0] = 0;
+  SQ_TRY(check_dtype(xt, fn));
+  if (gran != SQ_ACT_PER_TENSOR_STATIC && gran != SQ_ACT_PER_TOKEN_DYNAMIC &&
+      gran != SQ_ACT_PER_TENSOR_DYNAMIC)
+    return fail(SQ_ERR_INVALID_ARG, "%s: unknown granularity %d", fn, (int)gran);
+  if (T < 0) return fail(SQ_ERR_SHAPE, "%s: T=%lld < 0", fn, (long long)T);
+  SQ_TRY(check_k(K, fn));
+  SQ_REQ(x, fn);
+  SQ_REQ(residual, fn);
+  SQ_REQ(gamma_s, fn);
+  SQ_REQ(h, fn);
+  SQ_REQ(act_scale, fn);
+  SQ_REQ(xq, fn);
+  if (n_clipped && (((uintptr_t)n_clipped) & 7u))
+    return fail(SQ_ERR_ALIGN, "%s: n_clipped is not 8-byte aligned", fn);
+  if (!(eps >= 0.0f && isfinite(eps)))
+    return fail(SQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  if (T == 0) return SQ_OK;
+  const cudaStream_t st = (cudaStream_t)stream;
+  AddNormArgs a{};
+  a.x = x; a.res = residual; a.h = h; a.T = T; a.K = K; a.g = gamma_s; a.eps = eps;
+  a.scale = act_scale; a.q = xq; a.n_clipped = (unsigned long long*)n_clipped;
+  cudaError_t e;
+  if (gran != SQ_ACT_PER_TENSOR_DYNAMIC) {
+    e = launch_addnorm(a, xt, gran == SQ_ACT_PER_TOKEN_DYNAMIC ? ROW_DYNAMIC : ROW_STATIC, st);
+  } else {
+    // h and the call's peak, the step, then the static quantizer on h
+    a.peak = act_scale;
+    e = launch_zero(act_scale, sizeof(float), st);
+    if (e == cudaSuccess) e = launch_addnorm(a, xt, ROW_PEAK, st);
+    if (e == cudaSuccess) e = launch_peak_to_delta(act_scale, st);
+    RowArgs q{};
+    q.x = h; q.T = T; q.K = K; q.g = gamma_s; q.eps = eps; q.rms = 1;
+    q.scale = act_scale; q.q = xq; q.n_clipped = a.n_clipped;
+    if (e == cudaSuccess) e = launch_row(q, xt, ROW_STATIC, st);
+  }
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+namespace {
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;
+
+sq_status check_experts(int64_t E, const char* fn) {
+  if (E < 1 || E > kMaxExperts)
+    return fail(SQ_ERR_SHAPE, "%s: E=%lld must lie in [1, %d]", fn, (long long)E, kMaxExperts);
+  return SQ_OK;
+}
+sq_status check_routing(int64_t T, int64_t top_k, const char* fn) {
+  if (T < 0 || T > kMaxRows || top_k < 1 || top_k > kMaxRows || (T && top_k > kMaxRows / T))
+    return fail(SQ_ERR_SHAPE, "%s: T=%lld >= 0, top_k=%lld >= 1 and T * top_k < 2^31 are needed",
+                fn, (long long)T, (long long)top_k);
+  return SQ_OK;
+}
+sq_status check_rows(int64_t R, int64_t width, const char* fn) {
+  if (R < 0 || R > kMaxRows)
+    return fail(SQ_ERR_SHAPE, "%s: R=%lld must lie in [0, 2^31)", fn, (long long)R);
+  if (width < 1 || width > kMaxWidth)
+    return fail(SQ_ERR_SHAPE, "%s: a row width of %lld is outside [1, 2^20]", fn, (long long)width);
+  return SQ_OK;
+}
+}  // namespace
+
+size_t sq_moe_sort_workspace_bytes(int64_t T, int64_t top_k, int64_t E) {
+  if (T <= 0 || top_k < 1 || top_k > kMaxRows / T || E < 1 || E > kMaxExperts) return 0;
+  return moe_sort_workspace_bytes(T * top_k, (int)E);
+}
+
+sq_status sq_moe_sort(const void* expert_ids, sq_dtype it, int64_t T, int64_t top_k, int64_t E,
+                      int32_t* offsets, int32_t* pos, void* workspace, size_t workspace_bytes,
+                      sq_stream stream) {
+  const char* fn = "sq_moe_sort";
+  g_last_error[0] = 0;
+  if (it != SQ_I32 && it != SQ_I64)
+    return fail(SQ_ERR_DTYPE, "%s: expert ids are int32 or int64, not type %d", fn, (int)it);
+  SQ_TRY(check_routing(T, top_k, fn));
+  SQ_TRY(check_experts(E, fn));
+  SQ_REQ(offsets, fn);
+  if (T > 0) {
+    SQ_REQ(expert_ids, fn);
+    SQ_REQ(pos, fn);
+  }
+  const size_t need = sq_moe_sort_workspace_bytes(T, top_k, E);
+  if (need) {
+    if (!workspace || workspace_bytes < need)
+      return fail(SQ_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                  workspace ? workspace_bytes : (size_t)0);
+    SQ_OPT(workspace, fn);
+  }
+  const cudaError_t e = launch_moe_sort(expert_ids, it == SQ_I64, T * top_k, (int)E, offsets, pos,
+                                        workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+sq_status sq_moe_gather(const void* x, sq_dtype xt, int64_t T, int64_t K, const float* scale,
+                        const int32_t* pos, int64_t top_k, int64_t R, void* xs, float* scale_out,
+                        sq_stream stream) {
+  const char* fn = "sq_moe_gather";
+  g_last_error[0] = 0;
+  if (xt != SQ_I8 && xt != SQ_BF16 && xt != SQ_F32)
+    return fail(SQ_ERR_DTYPE, "%s: rows are int8, bf16 or fp32, not type %d", fn, (int)xt);
+  SQ_TRY(check_routing(T, top_k, fn));
+  SQ_TRY(check_rows(R, K, fn));
+  if (!scale != !scale_out)
+    return fail(SQ_ERR_INVALID_ARG, "%s: pass scale and scale_out together", fn);
+  if (T == 0 || R == 0) return SQ_OK;
+  SQ_REQ(x, fn);
+  SQ_REQ(pos, fn);
+  SQ_REQ(xs, fn);
+  SQ_OPT(scale, fn);
+  SQ_OPT(scale_out, fn);
+  MoeArgs a{};
+  a.x = x; a.pos = pos; a.scale = scale; a.scale_out = scale_out; a.out = xs;
+  a.T = T; a.R = R; a.N = K; a.top_k = (int)top_k;
+  const cudaError_t e = launch_moe_gather(a, xt == SQ_I8 ? 1 : xt == SQ_BF16 ? 2 : 4,
+                                          (cudaStream_t)stream);
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+sq_status sq_moe_combine(const void* z, sq_dtype t, int64_t R, int64_t N, const int32_t* pos,
+                         const float* w, int64_t T, int64_t top_k, const void* residual, void* y,
+                         sq_stream stream) {
+  const char* fn = "sq_moe_combine";
+  g_last_error[0] = 0;
+  SQ_TRY(check_dtype(t, fn));
+  SQ_TRY(check_routing(T, top_k, fn));
+  SQ_TRY(check_rows(R, N, fn));
+  if (T == 0) return SQ_OK;
+  if (R > 0) SQ_REQ(z, fn);
+  SQ_REQ(pos, fn);
+  SQ_OPT(w, fn);
+  SQ_OPT(residual, fn);
+  SQ_REQ(y, fn);
+  MoeArgs a{};
+  a.x = z; a.res = residual; a.pos = pos; a.w = w; a.out = y;
+  a.T = T; a.R = R; a.N = N; a.top_k = (int)top_k;
+  const cudaError_t e = launch_moe_combine(a, t, false, (cudaStream_t)stream);
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+sq_status sq_moe_combine_grad(const void* dy, sq_dtype t, int64_t T, int64_t N, const int32_t* pos,
+                              const float* w, int64_t top_k, const void* z, int64_t R, void* dz,
+                              float* dw, sq_stream stream) {
+  const char* fn = "sq_moe_combine_grad";
+  g_last_error[0] = 0;
+  SQ_TRY(check_dtype(t, fn));
+  SQ_TRY(check_routing(T, top_k, fn));
+  SQ_TRY(check_rows(R, N, fn));
+  if (T == 0 || (!dz && !dw)) return SQ_OK;
+  SQ_REQ(dy, fn);
+  SQ_REQ(pos, fn);
+  SQ_OPT(w, fn);
+  if (dw && R > 0) SQ_REQ(z, fn);
+  SQ_OPT(z, fn);
+  SQ_OPT(dz, fn);
+  SQ_OPT(dw, fn);
+  MoeArgs a{};
+  a.x = z; a.res = dy; a.pos = pos; a.w = w; a.out = dz; a.dw = dw;
+  a.T = T; a.R = R; a.N = N; a.top_k = (int)top_k;
+  const cudaError_t e = launch_moe_combine(a, t, true, (cudaStream_t)stream);
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+size_t sq_gemm_w8a8_grouped_workspace_bytes(int64_t R, int64_t N, int64_t K, int64_t E) {
+  if (R <= 0 || N <= 0 || K <= 0 || E <= 0) return 0;
+  return gemm_grouped_workspace_bytes(R, N, K, E);
+}
+
+sq_status sq_gemm_w8a8_grouped(const int8_t* xq, const int8_t* wq, const int32_t* offsets,
+                               int64_t R, int64_t N, int64_t K, int64_t E, const float* act_scale,
+                               int act_per_token, const float* w_scale, const float* bias, void* y,
+                               sq_dtype yt, int32_t* acc_out, void* workspace,
+                               size_t workspace_bytes, sq_stream stream) {
+  const char* fn = "sq_gemm_w8a8_grouped";
+  g_last_error[0] = 0;
+  SQ_TRY(check_dtype(yt, fn));
+  if (R < 0 || N < 0) return fail(SQ_ERR_SHAPE, "%s: R=%lld N=%lld must be >= 0", fn,
+                                  (long long)R, (long long)N);
+  SQ_TRY(check_k(K, fn));
+  SQ_TRY(check_experts(E, fn));
+  if (R == 0 || N == 0) return SQ_OK;
+  if (R > kMaxRows || N > kMaxRows || (R / 128 + E) > kMaxRows / ((N + 127) / 128))
+    return fail(SQ_ERR_SHAPE, "%s: (R / 128 + E) x (N / 128) tiles must stay below 2^31", fn);
+  SQ_REQ(xq, fn);
+  SQ_REQ(wq, fn);
+  SQ_REQ(offsets, fn);
+  SQ_REQ(act_scale, fn);
+  SQ_REQ(w_scale, fn);
+  SQ_OPT(bias, fn);
+  SQ_REQ(y, fn);
+  SQ_OPT(acc_out, fn);
+  const size_t need = gemm_grouped_workspace_bytes(R, N, K, E);
+  if (need) {
+    if (!workspace || workspace_bytes < need)
+      return fail(SQ_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                  workspace ? workspace_bytes : (size_t)0);
+    SQ_OPT(workspace, fn);
+  }
+  GroupArgs a{};
+  a.xq = xq; a.wq = wq; a.offsets = offsets; a.R = R; a.N = N; a.K = K; a.E = E;
+  a.act_scale = act_scale; a.act_per_token = act_per_token ? 1 : 0;
+  a.w_scale = w_scale; a.bias = bias; a.y = y; a.yt = yt; a.acc_out = acc_out;
+  a.workspace = workspace;
+  return launch_gemm_grouped(a, (cudaStream_t)stream);
+}
+
 size_t sq_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   return gemm_workspace_bytes(M, N, K);

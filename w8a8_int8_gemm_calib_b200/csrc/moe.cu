@@ -1,0 +1,446 @@
+// moe.cu -- tokens sorted by expert and back: the routing around a W8A8
+// linear whose weights are experts chosen per token.
+//
+//   sort     offsets[e] = #{i : id_i < e},  pos_i = offsets[id_i] +
+//            #{j < i : id_j = id_i}   over the live assignments i = (t, c)
+//   gather   xs[pos_i] = x[t]  (and its step)
+//   combine  y[t] = rnd(res[t] + sum_c w[t,c] z[pos_i])
+//   grad     dz[pos_i] = rnd(w[t,c] dy[t]),  dw[t,c] = sum_n dy[t,n] z[pos_i,n]
+//
+// Everything is indexed by token: a token's row is read once and its top_k
+// rows are written (gather, grad) or read (combine, grad), so no step needs
+// the inverse order, and every sum runs in one fixed order.
+//
+// Bound: HBM for the row steps -- the sort moves 12 bytes per assignment and
+// is bound by its launches.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "launch.cuh"
+#include "sq_device.cuh"
+#include "sq_internal.h"
+
+namespace sq {
+
+namespace {
+
+// ====================================================================== sort
+// A stable counting sort.  The assignments are cut into one contiguous part
+// per block and, within it, one contiguous run per warp.  A warp counts its
+// run by expert; an assignment's place is then the expert's offset, plus the
+// counts of the parts and runs before it, plus its rank in the run, which
+// the warp finds 32 assignments at a time by matching equal experts.  Counts
+// are integers, so the order the atomics run in changes nothing.
+constexpr int kSortWarps = 8;
+constexpr int kSortThreads = 32 * kSortWarps;
+constexpr int kSortSteps = 8;  // least steps of 32 per warp before blocks are added
+
+struct SortArgs {
+  const void* ids;
+  int ids64;
+  int64_t n, part;  // assignments, and those of a block (a multiple of kSortThreads)
+  int E, blocks;
+  int32_t* offsets;
+  int32_t* pos;
+  int32_t* counts;  // [blocks][E], when there are several blocks
+  unsigned int* status;
+};
+
+// expert of assignment i, or E when it goes to none
+__device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i) {
+  if (!in_bounds(i, 1, a.n, a.status)) return a.E;
+  const int64_t id = a.ids64 ? __ldcg(static_cast<const long long*>(a.ids) + i)
+                             : (int64_t)__ldcg(static_cast<const int*>(a.ids) + i);
+  return id >= 0 && id < a.E ? (int)id : a.E;
+}
+
+// cnt[warp][e] = the warp's assignments to e
+__device__ __forceinline__ void count_runs(const SortArgs& a, int* cnt, int64_t run0, int64_t run1) {
+  for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) cnt[i] = 0;
+  __syncthreads();
+  int* mine = cnt + (threadIdx.x >> 5) * a.E;
+  for (int64_t i = run0 + (threadIdx.x & 31); i < run1; i += 32) {
+    const int e = expert_of(a, i);
+    if (e < a.E) atomicAdd(mine + e, 1);
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void run_of(const SortArgs& a, int64_t& run0, int64_t& run1) {
+  const int64_t run = a.part / kSortWarps;
+  run0 = blockIdx.x * a.part + (threadIdx.x >> 5) * run;
+  run1 = run0 + run;
+  if (run1 > a.n) run1 = a.n;
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+  extern __shared__ int cnt[];
+  pdl_launch_dependents();
+  pdl_wait();
+  int64_t run0, run1;
+  run_of(a, run0, run1);
+  count_runs(a, cnt, run0, run1);
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) s += cnt[w * a.E + e];
+    const int64_t o = (int64_t)blockIdx.x * a.E + e;
+    if (in_bounds(o, 1, (int64_t)a.blocks * a.E, a.status)) a.counts[o] = s;
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs a) {
+  extern __shared__ int cnt[];        // [warps][E], then the experts' totals [E]
+  int* total = cnt + kSortWarps * a.E;
+  __shared__ int warp_sum[kSortWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t run0, run1;
+  run_of(a, run0, run1);
+  count_runs(a, cnt, run0, run1);
+  // totals over the call, and each run's start within its expert
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+    int before = 0, all = 0;
+    if (a.blocks > 1) {
+#pragma unroll 8
+      for (int b = 0; b < a.blocks; ++b) {
+        const int64_t o = (int64_t)b * a.E + e;
+        const int v = in_bounds(o, 1, (int64_t)a.blocks * a.E, a.status) ? __ldcg(a.counts + o) : 0;
+        all += v;
+        before += b < (int)blockIdx.x ? v : 0;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int v = cnt[w * a.E + e];
+      cnt[w * a.E + e] = before;
+      before += v;
+    }
+    total[e] = a.blocks > 1 ? all : before;
+  }
+  __syncthreads();
+  // exclusive sums of the totals: the offsets, added to every run's start
+  int carry = 0;
+  for (int e0 = 0; e0 < a.E; e0 += kSortThreads) {
+    const int e = e0 + threadIdx.x;
+    const int v = e < a.E ? total[e] : 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    int below = carry;
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) below += warp_sum[w];
+      carry += warp_sum[w];
+    }
+    const int off = below + s - v;
+    if (e < a.E) {
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) cnt[w * a.E + e] += off;
+      if (blockIdx.x == 0) a.offsets[e] = off;
+    }
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = carry;
+  // places, 32 assignments at a time in order
+  int* mine = cnt + warp * a.E;
+  for (int64_t i0 = run0; i0 < run1; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const int e = i < run1 ? expert_of(a, i) : a.E;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    int at = -1;
+    if (e < a.E) at = mine[e] + rank;
+    __syncwarp();
+    if (e < a.E && rank == 0) mine[e] += __popc(same);
+    __syncwarp();
+    if (i < run1 && in_bounds(i, 1, a.n, a.status)) a.pos[i] = at;
+  }
+}
+
+// Blocks: one up to kSortSteps steps of a warp (2048 assignments), then as
+// many as that leaves work for, one per SM at most (every block sums the
+// counts of all).
+int sort_blocks(int64_t n) {
+  const int64_t least = (int64_t)kSortThreads * kSortSteps;
+  const int64_t b = (n + least - 1) / least;
+  const int64_t most = sm_count();
+  return (int)(b < 1 ? 1 : b > most ? most : b);
+}
+
+// ====================================================================== rows
+// 16 bytes of a row, or one element where rows do not keep 16-byte alignment
+template <typename T, bool VEC> struct Lane;
+template <> struct Lane<uint16_t, true> {
+  static constexpr int V = 8;
+  uint4 a;
+  __device__ __forceinline__ void load(const uint16_t* p) { a = ld_stream_u4(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    Raw8<uint16_t> r;
+    r.a = a;
+    unpack(r, v);
+  }
+  static __device__ __forceinline__ void put(uint16_t* p, const float (&v)[8]) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      h[i] = *reinterpret_cast<uint32_t*>(&t);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+};
+template <> struct Lane<float, true> {
+  static constexpr int V = 4;
+  uint4 a;
+  __device__ __forceinline__ void load(const float* p) { a = ld_stream_u4(p); }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+    v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+  }
+  static __device__ __forceinline__ void put(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <> struct Lane<uint16_t, false> {
+  static constexpr int V = 1;
+  uint16_t a;
+  __device__ __forceinline__ void load(const uint16_t* p) { a = __ldcg(p); }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __uint_as_float((uint32_t)a << 16); }
+  static __device__ __forceinline__ void put(uint16_t* p, const float (&v)[1]) {
+    __nv_bfloat16 t = __float2bfloat16_rn(v[0]);
+    *p = *reinterpret_cast<uint16_t*>(&t);
+  }
+};
+template <> struct Lane<float, false> {
+  static constexpr int V = 1;
+  float a;
+  __device__ __forceinline__ void load(const float* p) { a = __ldcg(p); }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
+  static __device__ __forceinline__ void put(float* p, const float (&v)[1]) { *p = v[0]; }
+};
+
+constexpr int kRowThreads = 256;
+constexpr int kBatch = 8;  // assignments of a token whose rows are in flight together
+
+// the sorted row of assignment (t, c), or -1
+__device__ __forceinline__ int64_t place(const MoeArgs& a, int64_t t, int c) {
+  if (c >= a.top_k || !in_bounds(t * a.top_k + c, 1, a.T * a.top_k, a.status)) return -1;
+  const int64_t r = __ldcg(a.pos + t * a.top_k + c);
+  return r >= 0 && r < a.R ? r : -1;
+}
+
+// ---------------------------------------------------------------- gather
+// U: the unit a row is copied in (16 bytes, or its element)
+template <typename U>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const MoeArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t t = blockIdx.x;
+  const int64_t n = a.N;  // units per row
+  const int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
+  if (a.scale && c < a.top_k) {
+    for (int64_t k = c; k < a.top_k; k += (int64_t)gridDim.y * blockDim.x) {
+      const int64_t r = place(a, t, (int)k);
+      if (r >= 0 && in_bounds(t, 1, a.T, a.status)) a.scale_out[r] = __ldcg(a.scale + t);
+    }
+  }
+  if (c >= n || !in_bounds(t * n + c, 1, a.T * n, a.status)) return;
+  const U v = __ldcg(static_cast<const U*>(a.x) + t * n + c);
+  for (int k = 0; k < a.top_k; ++k) {
+    const int64_t r = place(a, t, k);
+    if (r >= 0 && in_bounds(r * n + c, 1, a.R * n, a.status)) static_cast<U*>(a.out)[r * n + c] = v;
+  }
+}
+
+// ---------------------------------------------------------------- combine
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const MoeArgs a) {
+  using L = Lane<T, VEC>;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t t = blockIdx.x;
+  const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * L::V;
+  if (c >= a.N) return;
+  const T* z = static_cast<const T*>(a.x);
+  float acc[L::V];
+  if (a.res && in_bounds(t * a.N + c, L::V, a.T * a.N, a.status)) {
+    L r;
+    r.load(static_cast<const T*>(a.res) + t * a.N + c);
+    r.get(acc);
+  } else {
+#pragma unroll
+    for (int e = 0; e < L::V; ++e) acc[e] = 0.0f;
+  }
+  for (int k0 = 0; k0 < a.top_k; k0 += kBatch) {
+    L raw[kBatch];
+    int64_t row[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      row[b] = place(a, t, k0 + b);
+      if (row[b] >= 0 && in_bounds(row[b] * a.N + c, L::V, a.R * a.N, a.status))
+        raw[b].load(z + row[b] * a.N + c);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (row[b] < 0) continue;
+      float v[L::V];
+      raw[b].get(v);
+      if (a.w) {
+        const float wt = __ldcg(a.w + t * a.top_k + k0 + b);
+#pragma unroll
+        for (int e = 0; e < L::V; ++e) acc[e] = __fmaf_rn(wt, v[e], acc[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < L::V; ++e) acc[e] = __fadd_rn(acc[e], v[e]);
+      }
+    }
+  }
+  if (in_bounds(t * a.N + c, L::V, a.T * a.N, a.status))
+    L::put(static_cast<T*>(a.out) + t * a.N + c, acc);
+}
+
+// ---------------------------------------------------------------- grad
+// One block per token.  Each thread adds its columns' products in increasing
+// column, the warps' lanes are combined by a butterfly and the warps in
+// order: one fixed order, fp32.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const MoeArgs a) {
+  using L = Lane<T, VEC>;
+  __shared__ float part[kRowThreads / 32][kBatch];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* dy = static_cast<const T*>(a.res);
+  const T* z = static_cast<const T*>(a.x);
+  T* dz = static_cast<T*>(a.out);
+  for (int k0 = 0; k0 < a.top_k; k0 += kBatch) {
+    int64_t row[kBatch];
+    float wt[kBatch], dot[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      row[b] = place(a, t, k0 + b);
+      wt[b] = row[b] >= 0 && a.w ? __ldcg(a.w + t * a.top_k + k0 + b) : 1.0f;
+      dot[b] = 0.0f;
+    }
+    for (int64_t c = (int64_t)threadIdx.x * L::V; c < a.N; c += (int64_t)blockDim.x * L::V) {
+      L zr[kBatch], dr;
+      if (!in_bounds(t * a.N + c, L::V, a.T * a.N, a.status)) break;
+      dr.load(dy + t * a.N + c);
+      if (a.dw) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (row[b] >= 0 && in_bounds(row[b] * a.N + c, L::V, a.R * a.N, a.status))
+            zr[b].load(z + row[b] * a.N + c);
+      }
+      float d[L::V];
+      dr.get(d);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (row[b] < 0) continue;
+        float v[L::V];
+        if (a.dw) {
+          zr[b].get(v);
+#pragma unroll
+          for (int e = 0; e < L::V; ++e) dot[b] = __fmaf_rn(d[e], v[e], dot[b]);
+        }
+        if (dz && in_bounds(row[b] * a.N + c, L::V, a.R * a.N, a.status)) {
+#pragma unroll
+          for (int e = 0; e < L::V; ++e) v[e] = __fmul_rn(wt[b], d[e]);
+          L::put(dz + row[b] * a.N + c, v);
+        }
+      }
+    }
+    if (!a.dw) continue;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1)
+        dot[b] = __fadd_rn(dot[b], __shfl_xor_sync(0xffffffffu, dot[b], o));
+      if (lane == 0) part[warp][b] = dot[b];
+    }
+    __syncthreads();
+    if (threadIdx.x < kBatch && k0 + (int)threadIdx.x < a.top_k &&
+        in_bounds(t * a.top_k + k0 + threadIdx.x, 1, a.T * a.top_k, a.status)) {
+      float s = 0.0f;
+      for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s = __fadd_rn(s, part[w][threadIdx.x]);
+      a.dw[t * a.top_k + k0 + threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+}
+
+unsigned row_threads(int64_t n) {
+  return n >= kRowThreads ? (unsigned)kRowThreads : (unsigned)((n + 31) / 32 * 32);
+}
+
+template <typename T>
+cudaError_t launch_combine_t(const MoeArgs& a, bool grad, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const bool vec = a.N % V == 0;
+  const int64_t n = vec ? a.N / V : a.N;
+  const unsigned nt = row_threads(n);
+  if (grad)
+    return vec ? launch_pdl(combine_grad_kernel<T, true>, dim3((unsigned)a.T), dim3(nt), 0, st, a)
+               : launch_pdl(combine_grad_kernel<T, false>, dim3((unsigned)a.T), dim3(nt), 0, st, a);
+  const dim3 grid((unsigned)a.T, (unsigned)((n + nt - 1) / nt));
+  return vec ? launch_pdl(combine_kernel<T, true>, grid, dim3(nt), 0, st, a)
+             : launch_pdl(combine_kernel<T, false>, grid, dim3(nt), 0, st, a);
+}
+
+}  // namespace
+
+size_t moe_sort_workspace_bytes(int64_t n, int E) {
+  const int b = sort_blocks(n);
+  return b > 1 ? (size_t)b * (size_t)E * sizeof(int32_t) : 0;
+}
+
+cudaError_t launch_moe_sort(const void* ids, bool ids64, int64_t n, int E, int32_t* offsets,
+                            int32_t* pos, void* workspace, cudaStream_t st) {
+  SortArgs a{};
+  a.ids = ids; a.ids64 = ids64; a.n = n; a.E = E;
+  a.blocks = sort_blocks(n);
+  const int64_t part = (n + a.blocks - 1) / a.blocks;
+  a.part = (part + kSortThreads - 1) / kSortThreads * kSortThreads;
+  a.offsets = offsets; a.pos = pos;
+  a.counts = static_cast<int32_t*>(workspace);
+  a.status = status_word();
+  if (!a.status) return cudaErrorInvalidDevice;
+  const size_t smem = (size_t)kSortWarps * E * sizeof(int);
+  if (a.blocks > 1) {
+    const cudaError_t e = launch_pdl(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads), smem,
+                                     st, a);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(sort_place_kernel, dim3(a.blocks), dim3(kSortThreads),
+                    smem + (size_t)E * sizeof(int), st, a);
+}
+
+cudaError_t launch_moe_gather(MoeArgs a, size_t elem, cudaStream_t st) {
+  a.status = status_word();
+  if (!a.status) return cudaErrorInvalidDevice;
+  const bool vec = (size_t)a.N * elem % 16 == 0;
+  if (vec) a.N = (int64_t)((size_t)a.N * elem / 16);
+  const unsigned nt = row_threads(a.N);
+  const dim3 grid((unsigned)a.T, (unsigned)((a.N + nt - 1) / nt));
+  if (vec) return launch_pdl(gather_kernel<uint4>, grid, dim3(nt), 0, st, a);
+  if (elem == 1) return launch_pdl(gather_kernel<uint8_t>, grid, dim3(nt), 0, st, a);
+  if (elem == 2) return launch_pdl(gather_kernel<uint16_t>, grid, dim3(nt), 0, st, a);
+  return launch_pdl(gather_kernel<uint32_t>, grid, dim3(nt), 0, st, a);
+}
+
+cudaError_t launch_moe_combine(MoeArgs a, sq_dtype t, bool grad, cudaStream_t st) {
+  a.status = status_word();
+  if (!a.status) return cudaErrorInvalidDevice;
+  return t == SQ_BF16 ? launch_combine_t<uint16_t>(a, grad, st)
+                      : launch_combine_t<float>(a, grad, st);
+}
+
+}  // namespace sq

@@ -100,6 +100,48 @@ cudaError_t launch_fold_ln(const float* gamma, const float* beta,
                            const float* s, int64_t K, float* gamma_out,
                            float* beta_out, cudaStream_t st);
 
+// Residual addition + RMSNorm + quantizer (addnorm.cu).  ROW_PEAK writes h
+// and folds the peak of |y| into *peak; the codes then come from launch_row on h.
+struct AddNormArgs {
+  const void* x;
+  const void* res;
+  void* h;
+  int64_t T, K;
+  const float* g;
+  float eps;
+  float* scale;   // ROW_DYNAMIC: out [T]; ROW_STATIC: in [1]
+  int8_t* q;
+  unsigned long long* n_clipped;  // may be NULL
+  float* peak;    // ROW_PEAK: running peak [1] (fp32 bits, atomic max)
+  unsigned int* status;           // set by launch_addnorm
+};
+cudaError_t launch_addnorm(AddNormArgs a, sq_dtype xt, RowMode mode, cudaStream_t st);
+
+// ---------------------------------------------------------------- routing
+constexpr int kMaxExperts = 1024;
+
+size_t moe_sort_workspace_bytes(int64_t n, int E);
+cudaError_t launch_moe_sort(const void* ids, bool ids64, int64_t n, int E, int32_t* offsets,
+                            int32_t* pos, void* workspace, cudaStream_t st);
+
+// Row steps of the routing (moe.cu), by token t and assignment c; pos < 0 or
+// >= R: no row.
+struct MoeArgs {
+  const void* x;       // gather: tokens [T,N]; combine, grad: sorted rows z [R,N]
+  const void* res;     // combine: residual [T,N] or NULL; grad: dy [T,N]
+  const int32_t* pos;  // [T, top_k]
+  const float* w;      // [T, top_k] or NULL (1)
+  const float* scale;  // gather: [T] or NULL
+  float* scale_out;    // gather: [R]
+  void* out;           // gather: [R,N]; combine: [T,N]; grad: dz [R,N] or NULL
+  float* dw;           // grad: [T, top_k] or NULL
+  int64_t T, R, N;
+  int top_k;
+  unsigned int* status;  // set by the launch
+};
+cudaError_t launch_moe_gather(MoeArgs a, size_t elem_bytes, cudaStream_t st);
+cudaError_t launch_moe_combine(MoeArgs a, sq_dtype t, bool grad, cudaStream_t st);
+
 // ---------------------------------------------------------------- GEMM
 struct GemmArgs {
   const int8_t* xq;
@@ -132,6 +174,25 @@ struct BmmArgs {
   int32_t* acc_out;
 };
 sq_status launch_bmm(const BmmArgs& a, cudaStream_t st);
+
+// Grouped INT8 GEMM: rows offsets[e] .. offsets[e+1] - 1 of xq and y use
+// wq[e]; w_scale, bias [E, N]; offsets [E + 1] on the device.
+struct GroupArgs {
+  const int8_t* xq;
+  const int8_t* wq;
+  const int32_t* offsets;
+  int64_t R, N, K, E;
+  const float* act_scale;
+  int act_per_token;
+  const float* w_scale;
+  const float* bias;  // [E, N] or NULL
+  void* y;
+  sq_dtype yt;
+  int32_t* acc_out;
+  void* workspace;
+};
+size_t gemm_grouped_workspace_bytes(int64_t R, int64_t N, int64_t K, int64_t E);
+sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st);
 
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 sq_status launch_gemm(const GemmArgs& a, cudaStream_t st);
