@@ -22,6 +22,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "launch.cuh"
 #include "sq_device.cuh"
 #include "sq_internal.h"
@@ -31,12 +33,6 @@ namespace sq {
 namespace {
 
 constexpr int kSlice = 128;  // threads per row: the 128 reduction slots
-constexpr int kSlices = 4;   // rows a CTA works on at a time
-constexpr int kThreads = kSlice * kSlices;
-
-__device__ __forceinline__ void slice_bar(int slice) {
-  asm volatile("bar.sync %0, %1;" ::"r"(slice + 1), "r"(kSlice) : "memory");
-}
 
 // h = x + r of one chunk, rounded to the storage type and packed in it.
 __device__ __forceinline__ void add_chunk(const Raw8<float>& x, const Raw8<float>& r,
@@ -65,92 +61,117 @@ __device__ __forceinline__ void store_chunk(uint16_t* p, const Raw8<uint16_t>& h
 }
 
 // CM > 0: a thread's chunks of h (at most CM) stay in registers in their
-// storage form.  CM == 0: h is read back from global memory, each chunk by
-// the thread that wrote it.
+// storage form, its gamma in shared memory, and the next row's x and r are
+// loaded while this row is reduced and quantized.  CM == 0: h is read back
+// from global memory, each chunk by the thread that wrote it.
+//
+// A CTA is one 128-thread slice, so rows in different phases share an SM.
 template <typename T, int CM, int MODE>
-__global__ void __launch_bounds__(kThreads) addnorm_kernel(const AddNormArgs a) {
-  __shared__ float red[kSlices][2][4];
+__global__ void __launch_bounds__(kSlice) addnorm_kernel(const AddNormArgs a) {
+  __shared__ float red[2][4];
+  extern __shared__ __align__(16) float gs[];  // CM > 0: [2 CM][128] float4
   pdl_launch_dependents();
   pdl_wait();
-  const int slice = threadIdx.x / kSlice, j = threadIdx.x % kSlice;
-  const int w = j >> 5, lane = j & 31;
+  const int j = threadIdx.x, w = j >> 5, lane = j & 31;
   const int64_t K = a.K, nchunk = K >> 3, size = a.T * a.K;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.res);
   T* hp = static_cast<T*>(a.h);
   const float kf = (float)K;
-  const float static_inv = MODE == ROW_STATIC ? __fdiv_rn(1.0f, __ldcg(a.scale)) : 0.0f;
   unsigned clipped = 0;
   float peak = 0.0f;
 
-  for (int64_t row = blockIdx.x + (int64_t)slice * gridDim.x; row < a.T;
-       row += (int64_t)gridDim.x * kSlices) {
+  constexpr int C = CM > 0 ? CM : 1;
+  Raw8<T> xv[C], rv[C], h[C];
+  auto load_rows = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < CM; ++i) {
+      const int64_t c = j + i * kSlice, o = row * K + c * 8;
+      if (c < nchunk && row < a.T && in_bounds(o, 8, size, a.status)) {
+        load_raw(x + o, xv[i]);
+        load_raw(res + o, rv[i]);
+      }
+    }
+  };
+  if constexpr (CM > 0) {
+    load_rows(blockIdx.x);
+    // the thread's own chunks of gamma: written and read by it alone
+#pragma unroll
+    for (int i = 0; i < CM; ++i) {
+      const int64_t c = j + i * kSlice;
+      if (c < nchunk) {
+        float4* d = reinterpret_cast<float4*>(gs) + 2 * i * kSlice + j;
+        d[0] = __ldcg(reinterpret_cast<const float4*>(a.g + c * 8));
+        d[kSlice] = __ldcg(reinterpret_cast<const float4*>(a.g + c * 8) + 1);
+      }
+    }
+  }
+  const float static_inv = MODE == ROW_STATIC ? __fdiv_rn(1.0f, __ldcg(a.scale)) : 0.0f;
+
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const int64_t base = row * K;
-    Raw8<T> h[CM > 0 ? CM : 1];
     float p = 0.0f;
     // h = x + r, stored, and its sum of squares
-    auto first = [&](int64_t c, const Raw8<T>& xv, const Raw8<T>& rv, Raw8<T>& hv) {
-      add_chunk(xv, rv, hv);
-      if (in_bounds(base + c * 8, 8, size, a.status)) store_chunk(hp + base + c * 8, hv);
+    auto first = [&](int64_t c, const Raw8<T>& xc, const Raw8<T>& rc, Raw8<T>& hc) {
+      add_chunk(xc, rc, hc);
+      if (in_bounds(base + c * 8, 8, size, a.status)) store_chunk(hp + base + c * 8, hc);
       float v[8];
-      unpack(hv, v);
+      unpack(hc, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) p = __fmaf_rn(v[e], v[e], p);
     };
     if constexpr (CM > 0) {
-      Raw8<T> xv[CM], rv[CM];
 #pragma unroll
       for (int i = 0; i < CM; ++i) {
-        const int64_t c = j + (int64_t)i * kSlice;
-        if (c < nchunk && in_bounds(base + c * 8, 8, size, a.status)) {
-          load_raw(x + base + c * 8, xv[i]);
-          load_raw(res + base + c * 8, rv[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < CM; ++i) {
-        const int64_t c = j + (int64_t)i * kSlice;
+        const int64_t c = j + i * kSlice;
         if (c < nchunk) first(c, xv[i], rv[i], h[i]);
       }
+      load_rows(row + gridDim.x);
     } else {
       for (int64_t c = j; c < nchunk; c += kSlice) {
-        Raw8<T> xv{}, rv{}, hv;
+        Raw8<T> xc{}, rc{}, hc;
         if (in_bounds(base + c * 8, 8, size, a.status)) {
-          load_raw(x + base + c * 8, xv);
-          load_raw(res + base + c * 8, rv);
+          load_raw(x + base + c * 8, xc);
+          load_raw(res + base + c * 8, rc);
         }
-        first(c, xv, rv, hv);
+        first(c, xc, rc, hc);
       }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) p = __fadd_rn(p, __shfl_xor_sync(0xffffffffu, p, o));
-    if (lane == 0) red[slice][0][w] = p;
-    slice_bar(slice);
-    const float ss = __fadd_rn(__fadd_rn(red[slice][0][0], red[slice][0][2]),
-                               __fadd_rn(red[slice][0][1], red[slice][0][3]));
+    if (lane == 0) red[0][w] = p;
+    __syncthreads();
+    const float ss = __fadd_rn(__fadd_rn(red[0][0], red[0][2]), __fadd_rn(red[0][1], red[0][3]));
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, kf), a.eps)));
 
     // f(c, y[8]) over the thread's chunks
     auto each_y = [&](auto&& f) {
-      auto lift = [&](int64_t c, const Raw8<T>& hv) {
-        float v[8], g[8];
-        unpack(hv, v);
-        load8(a.g + c * 8, g);
+      auto lift = [&](int64_t c, const Raw8<T>& hc, const float (&g)[8]) {
+        float v[8];
+        unpack(hc, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], rstd), g[e]);
         f(c, v);
       };
+      float g[8];
       if constexpr (CM > 0) {
 #pragma unroll
         for (int i = 0; i < CM; ++i) {
-          const int64_t c = j + (int64_t)i * kSlice;
-          if (c < nchunk) lift(c, h[i]);
+          const int64_t c = j + i * kSlice;
+          if (c < nchunk) {
+            const float4* s = reinterpret_cast<const float4*>(gs) + 2 * i * kSlice + j;
+            const float4 u = s[0], v = s[kSlice];
+            g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w;
+            g[4] = v.x; g[5] = v.y; g[6] = v.z; g[7] = v.w;
+            lift(c, h[i], g);
+          }
         }
       } else {
         for (int64_t c = j; c < nchunk; c += kSlice) {
-          Raw8<T> hv{};
-          if (in_bounds(base + c * 8, 8, size, a.status)) load_raw_cached(hp + base + c * 8, hv);
-          lift(c, hv);
+          Raw8<T> hc{};
+          if (in_bounds(base + c * 8, 8, size, a.status)) load_raw_cached(hp + base + c * 8, hc);
+          load8(a.g + c * 8, g);
+          lift(c, hc, g);
         }
       }
     };
@@ -160,34 +181,33 @@ __global__ void __launch_bounds__(kThreads) addnorm_kernel(const AddNormArgs a) 
 #pragma unroll
         for (int e = 0; e < 8; ++e) peak = fmaxf(peak, fabsf(y[e]));
       });
-      slice_bar(slice);  // red is read by all before the next row writes it
-      continue;
-    }
-    if constexpr (MODE == ROW_DYNAMIC) {
-      float m = 0.0f;  // fmaxf: NaN elements are skipped
-      each_y([&](int64_t, const float (&y)[8]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
-      });
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane == 0) red[slice][1][w] = m;
-      slice_bar(slice);
-      m = fmaxf(fmaxf(red[slice][1][0], red[slice][1][2]),
-                fmaxf(red[slice][1][1], red[slice][1][3]));
-      const float delta = __fdiv_rn(fmaxf(m, 1e-7f), 127.0f);
-      inv = __fdiv_rn(1.0f, delta);
-      if (j == 0 && in_bounds(row, 1, a.T, a.status)) a.scale[row] = delta;
     } else {
-      slice_bar(slice);
-    }
-    const bool count = a.n_clipped != nullptr;
-    each_y([&](int64_t c, const float (&y)[8]) {
-      uint32_t b[8];
+      if constexpr (MODE == ROW_DYNAMIC) {
+        float m = 0.0f;  // fmaxf: NaN elements are skipped
+        each_y([&](int64_t, const float (&y)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = qbits(y[e], inv, count, clipped);
-      if (in_bounds(base + c * 8, 8, size, a.status)) store_codes(a.q + base + c * 8, b);
-    });
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+        });
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) red[1][w] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(red[1][0], red[1][2]), fmaxf(red[1][1], red[1][3]));
+        const float delta = __fdiv_rn(fmaxf(m, 1e-7f), 127.0f);
+        inv = __fdiv_rn(1.0f, delta);
+        if (j == 0 && in_bounds(row, 1, a.T, a.status)) a.scale[row] = delta;
+      }
+      const bool count = a.n_clipped != nullptr;
+      each_y([&](int64_t c, const float (&y)[8]) {
+        uint32_t b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] = qbits(y[e], inv, count, clipped);
+        if (in_bounds(base + c * 8, 8, size, a.status)) store_codes(a.q + base + c * 8, b);
+      });
+    }
+    // the next row's sum of squares overwrites red[0], which every warp read
+    // before the barrier of the peak (or reads before this one)
+    if constexpr (MODE != ROW_DYNAMIC) __syncthreads();
   }
   if constexpr (MODE == ROW_PEAK) {
 #pragma unroll
@@ -200,11 +220,25 @@ __global__ void __launch_bounds__(kThreads) addnorm_kernel(const AddNormArgs a) 
   }
 }
 
+// As many CTAs as are resident at once walk the rows.
 template <typename T, int CM, int MODE>
 cudaError_t launch_t(const AddNormArgs& a, cudaStream_t st) {
-  int64_t grid = 4 * (int64_t)sm_count();
+  auto kern = addnorm_kernel<T, CM, MODE>;
+  constexpr size_t smem = (size_t)CM * 8 * kSlice * sizeof(float);
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  static int per_sm[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    err[dev] = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm[dev], kern, kSlice, smem);
+  });
+  if (err[dev] != cudaSuccess) return err[dev];
+  int64_t grid = (int64_t)per_sm[dev] * sm_count();
+  if (grid < 1) return cudaErrorInvalidConfiguration;
   if (grid > a.T) grid = a.T;
-  return launch_pdl(addnorm_kernel<T, CM, MODE>, dim3((unsigned)grid), dim3(kThreads), 0, st, a);
+  return launch_pdl(kern, dim3((unsigned)grid), dim3(kSlice), smem, st, a);
 }
 
 template <typename T, int MODE>
