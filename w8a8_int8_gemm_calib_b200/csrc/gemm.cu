@@ -30,6 +30,7 @@
 #include "sq_device.cuh"
 #include "sq_internal.h"
 #include "tc_ptx.cuh"
+#include "tmaps.h"
 
 namespace sq {
 
@@ -72,9 +73,8 @@ struct TcCfg {
   static constexpr int STAGES = (224 * 1024 - 2048 - EPI_BYTES) / STAGE;
   static constexpr uint32_t TMEM_COLS = 2 * TBN <= 256 ? 256 : 512;  // power of two
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + EPI_BYTES + 256;
-  static constexpr size_t SMEM_GROUP = SMEM + 2 * (kMaxExperts + 1) * sizeof(int);  // + its table
   static_assert(STAGES >= 2, "two main-loop stages at least");
-  static_assert(SMEM_GROUP <= 227 * 1024, "shared memory");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 struct Params {
@@ -96,47 +96,7 @@ struct Params {
   // (2 per epilogue warp of every CTA); y is not written
   const float* err_ref;
   double* err_part;
-  // grouped: the experts' row offsets [E + 1] on the device
-  const int32_t* offsets;
-  int E;
 };
-
-// Grouped GEMM: the CTA's table of the experts' rows and row tiles, in
-// shared memory behind the barriers: off[E + 1], then tiles[E + 1] (row
-// tiles before expert e).
-// One warp fills the table.  Offsets outside [0, rows] or falling ones are
-// clamped to a rising sequence, so a bad table gives wrong rows to experts
-// but no tile outside the rows.
-__device__ __forceinline__ void group_table(const int32_t* offsets, int E, int rows, int tile_m,
-                                            int* off, int* tiles) {
-  const int lane = threadIdx.x & 31;
-  int top = 0, before = 0;
-  for (int e0 = 0; e0 <= E; e0 += 32) {
-    const int e = e0 + lane;
-    int v = e <= E ? min(max(__ldcg(offsets + e), 0), rows) : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v = max(v, u);
-    }
-    v = max(v, top);
-    const int prev = __shfl_up_sync(0xffffffffu, v, 1);
-    // row tiles of expert e - 1: the rows between offsets e - 1 and e
-    const int n = e > 0 && e <= E ? (v - (lane ? prev : top) + tile_m - 1) / tile_m : 0;
-    int s = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (e <= E) {
-      off[e] = v;
-      tiles[e] = before + s;
-    }
-    top = __shfl_sync(0xffffffffu, v, 31);
-    before += __shfl_sync(0xffffffffu, s, 31);
-  }
-}
 
 __device__ __forceinline__ void tile_coords(int tile, int m_tiles, int n_tiles, int& mb, int& nb,
                                             int group_m = GROUP_M) {
@@ -175,17 +135,16 @@ __device__ __forceinline__ float dequant(uint32_t acc, float as, float ws) {
 // weight step, wt = w_scale[b].  They are loaded before the chunk's
 // accumulators, so that their L2 latency overlaps the TMEM load (measured:
 // 16384 x 28672 x 8192 2382 -> 2264 us, attention scores 94.2 -> 92.2 us).
-// Grouped: b is the expert, with its own row of w_scale and bias.
-template <bool BATCH, bool GROUP>
+template <bool BATCH>
 __device__ __forceinline__ void load_scales(const Params& p, int b, int col0, float wt,
                                             float (&ws)[32], float (&bs)[32]) {
   if (BATCH && p.w_per_tensor) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) ws[i] = wt;
   } else {
-    load_cols32(p.w_scale + (BATCH || GROUP ? (size_t)b * (size_t)p.N : (size_t)0), col0, p.N, ws);
+    load_cols32(p.w_scale + (BATCH ? (size_t)b * (size_t)p.N : (size_t)0), col0, p.N, ws);
   }
-  if (p.bias) load_cols32(p.bias + (GROUP ? (size_t)b * (size_t)p.N : (size_t)0), col0, p.N, bs);
+  if (p.bias) load_cols32(p.bias, col0, p.N, bs);
 }
 // The 32 outputs of one row: (float)acc * (as * ws[n]) (+ bias[n])
 __device__ __forceinline__ void dequant_loaded(const Params& p, const uint32_t (&r)[32], float as,
@@ -262,20 +221,11 @@ __device__ __forceinline__ void store_chunk(const Params& p, size_t yrow, int co
 // stage barriers, the even CTA's commits arrive on both CTAs' barriers, and
 // both CTAs' epilogue warps release the accumulator on the even CTA's
 // barrier.  No load is multicast.
-//
-// GROUP: the experts' GEMM.  The rows of A and y are grouped by expert
-// (offsets on the device), B is [E, N, K]; every CTA works the tile list out
-// of the offsets, an expert's tiles in a row.  A row tile starts at its
-// expert's first row, wherever that is (a TMA row coordinate has no
-// alignment rule), and may load rows of the next expert, whose outputs are
-// not stored.
-template <bool BF16, int TBN, bool BATCH, int EPI_NB, int EPI_W, bool ERR, bool PAIR = false,
-          bool GROUP = false>
+template <bool BF16, int TBN, bool BATCH, int EPI_NB, int EPI_W, bool ERR, bool PAIR = false>
 __global__ void __launch_bounds__(TcCfg<TBN, EPI_NB, EPI_W, PAIR>::THREADS, 1)
 gemm_w8a8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmY, const Params p) {
   static_assert(!PAIR || (!BATCH && !ERR), "CTA pairs serve the plain GEMM");
-  static_assert(!GROUP || (!BATCH && !ERR), "grouped rows are not batched");
   using C = TcCfg<TBN, EPI_NB, EPI_W, PAIR>;
   constexpr int TILE_M = C::TILE_M;
   constexpr int B_ROWS = C::B_ROWS;
@@ -340,43 +290,15 @@ gemm_w8a8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();  // the prologue above touches no global memory
 
-  // grouped: the row tiles of every expert, and the number of tiles
-  int* g_off = reinterpret_cast<int*>(sEpi + C::EPI_BYTES + 256);
-  int* g_tiles = g_off + (kMaxExperts + 1);
-  int num_tiles = p.num_tiles;
-  if constexpr (GROUP) {
-    if (warp == 0) group_table(p.offsets, p.E, p.M, TILE_M, g_off, g_tiles);
-    __syncthreads();
-    num_tiles = g_tiles[p.E] * p.n_tiles;
-  }
-  // b: the tile's batch, or its expert (tiles ascend: the search goes on from
-  // the last one's); row_a: its first row of A and y; row_end: one past its
-  // group's last row
-  auto locate = [&](int tile, int& b, int& nb, int& row_a, int& row_end) {
-    int mb;
-    if constexpr (GROUP) {
-      while (tile >= g_tiles[b + 1] * p.n_tiles) ++b;
-      tile_coords(tile - g_tiles[b] * p.n_tiles, g_tiles[b + 1] - g_tiles[b], p.n_tiles, mb, nb,
-                  p.group);
-      row_a = g_off[b] + mb * TILE_M;
-      row_end = g_off[b + 1];
-    } else {
-      b = BATCH ? tile / p.tiles_per_batch : 0;
-      tile_coords(tile - b * p.tiles_per_batch, p.m_tiles, p.n_tiles, mb, nb, p.group);
-      row_a = mb * TILE_M;
-      row_end = p.M;
-    }
-  };
-
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (tc::elect_one()) {
       uint32_t stage = 0, phase = 0, issued = 0, issued_par = 0;
       bool ok = true;
-      int b = 0;
-      for (int tile = unit0; ok && tile < num_tiles; tile += units) {
-        int nb, row_a, row_end;
-        locate(tile, b, nb, row_a, row_end);
+      for (int tile = unit0; ok && tile < p.num_tiles; tile += units) {
+        int mb, nb;
+        const int b = BATCH ? tile / p.tiles_per_batch : 0;
+        tile_coords(tile - b * p.tiles_per_batch, p.m_tiles, p.n_tiles, mb, nb, p.group);
         for (int kb = 0; kb < p.nk; ++kb) {
           if (!tc::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, kWaitNs, p.status)) {
             ok = false;
@@ -388,13 +310,9 @@ gemm_w8a8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             const uint32_t fb = tc::mapa_shared(full_bar(stage), 0);
             if (leader) tc::mbar_arrive_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
             tc::tma_load_2d_pair(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BK,
-                                 row_a + (int)rank * BM, fb);
-            if constexpr (GROUP)
-              tc::tma_load_3d_pair(tc::smem_u32(sB + stage * B_BYTES), &tmB, kb * BK,
-                                   nb * BN + (int)rank * B_ROWS, b, fb);
-            else
-              tc::tma_load_2d_pair(tc::smem_u32(sB + stage * B_BYTES), &tmB, kb * BK,
-                                   nb * BN + (int)rank * B_ROWS, fb);
+                                 mb * TILE_M + (int)rank * BM, fb);
+            tc::tma_load_2d_pair(tc::smem_u32(sB + stage * B_BYTES), &tmB, kb * BK,
+                                 nb * BN + (int)rank * B_ROWS, fb);
             issued |= 1u << stage;
             issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -402,17 +320,12 @@ gemm_w8a8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           }
           tc::mbar_arrive_expect_tx(full_bar(stage), STAGE_BYTES);
           if constexpr (BATCH) {
-            tc::tma_load_3d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BK, row_a, b,
-                            full_bar(stage));
-            tc::tma_load_3d(tc::smem_u32(sB + stage * B_BYTES), &tmB, kb * BK, nb * BN, b,
-                            full_bar(stage));
-          } else if constexpr (GROUP) {
-            tc::tma_load_2d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BK, row_a,
+            tc::tma_load_3d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BK, mb * BM, b,
                             full_bar(stage));
             tc::tma_load_3d(tc::smem_u32(sB + stage * B_BYTES), &tmB, kb * BK, nb * BN, b,
                             full_bar(stage));
           } else {
-            tc::tma_load_2d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BK, row_a,
+            tc::tma_load_2d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BK, mb * BM,
                             full_bar(stage));
             tc::tma_load_2d(tc::smem_u32(sB + stage * B_BYTES), &tmB, kb * BK, nb * BN,
                             full_bar(stage));
@@ -445,7 +358,7 @@ gemm_w8a8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       constexpr uint32_t idesc = tc::idesc_i8(TILE_M, BN);
       uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
       bool ok = true;
-      for (int tile = unit0; ok && tile < num_tiles; tile += units) {
+      for (int tile = unit0; ok && tile < p.num_tiles; tile += units) {
         if (!tc::mbar_wait(tempty_bar(abuf), aphase ^ 1u, abort_flag, kWaitNs, p.status)) {
           ok = false;
           break;
@@ -497,26 +410,25 @@ gemm_w8a8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     uint32_t nstore = 0;  // TMA stores issued by this warp (selects the buffer)
     double e_num = 0.0, e_den = 0.0;  // error mode: this lane's sums
     uint32_t abuf = 0, aphase = 0;
-    int b = 0;
-    for (int tile = unit0; tile < num_tiles; tile += units) {
-      int nb, row_a, row_end;
-      locate(tile, b, nb, row_a, row_end);
+    for (int tile = unit0; tile < p.num_tiles; tile += units) {
+      int mb, nb;
+      const int b = BATCH ? tile / p.tiles_per_batch : 0;
+      tile_coords(tile - b * p.tiles_per_batch, p.m_tiles, p.n_tiles, mb, nb, p.group);
       if (!tc::mbar_wait(tfull_bar(abuf), aphase, abort_flag, kWaitNs, p.status)) break;
       tc::tc_fence_after();
-      const int row0 = row_a + (int)rank * BM + quarter * 32;
+      const int row0 = mb * TILE_M + (int)rank * BM + quarter * 32;
       const int row = row0 + lane;
-      const bool row_ok = row < row_end;
-      // output row of [batch*M, N]
-      const size_t yrow = (size_t)(BATCH ? b : 0) * (size_t)p.M + (size_t)row;
+      const bool row_ok = row < p.M;
+      const size_t yrow = (size_t)b * (size_t)p.M + (size_t)row;  // output row of [batch*M, N]
       const float as = p.per_token ? (row_ok ? __ldcg(p.act_scale + yrow) : 0.0f)
-                                   : __ldcg(p.act_scale + (BATCH ? b : 0));
+                                   : __ldcg(p.act_scale + b);
       const uint32_t taddr = tmem_base + abuf * BN + ((uint32_t)(quarter * 32) << 16);
       const float wt = (BATCH && p.w_per_tensor) ? __ldcg(p.w_scale + b) : 0.0f;
 #pragma unroll 1
       for (int c = chunk0; c < BN / 32; c += EPI_W / 4) {
         const int col0 = nb * BN + c * 32;
         float ws[32], bs[32];
-        load_scales<BATCH, GROUP>(p, b, col0, wt, ws, bs);  // in flight during the TMEM load
+        load_scales<BATCH>(p, b, col0, wt, ws, bs);  // in flight during the TMEM load
         uint32_t r[32];
         tc::tmem_ld32(taddr + c * 32, r);
         tc::tmem_ld_wait();
@@ -539,9 +451,7 @@ gemm_w8a8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           }
           continue;
         }
-        // a TMA store clips at the tensor's edge, not at the group's: the
-        // group's last rows go by plain stores
-        if (!p.tma_store || (GROUP && row0 + 32 > row_end)) {
+        if (!p.tma_store) {
           if (row_ok && col0 < p.N) store_chunk<BF16>(p, yrow, col0, r, yv);
           continue;
         }
@@ -937,7 +847,11 @@ gemm_w8a8_smallm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_co
   }
 }
 
+}  // namespace
+
 // ------------------------------------------------------------------ host side
+// Tensor maps (tmaps.h: the grouped GEMM takes them too).
+namespace {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
@@ -952,6 +866,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return g_encode;
 }
+}  // namespace
 
 // 2-D int8 tensor [rows, inner] (row stride = inner bytes), box
 // [box_rows, 128 bytes], 128-byte swizzle, zero fill out of bounds.
@@ -969,19 +884,20 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, 
 }
 
 // Output tensor map for the TMA-store epilogue: [rows, cols] of bf16/fp32,
-// box 64 bytes x 32 rows, 64-byte swizzle.
-bool make_tmap_out(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, bool bf16) {
+// box row_bytes (64 or 128) x 32 rows, swizzled over those bytes.
+bool make_tmap_out(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, bool bf16,
+                   uint32_t row_bytes) {
   auto enc = encode_fn();
   if (!enc) return false;
   const uint64_t esz = bf16 ? 2 : 4;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * esz};
-  cuuint32_t box[2] = {(cuuint32_t)(64 / esz), 32};
+  cuuint32_t box[2] = {(cuuint32_t)(row_bytes / esz), 32};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
                    base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -1001,6 +917,7 @@ bool make_tmap3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+namespace {
 // Batched output [batch, rows, cols]: stores clipped at each batch's edges.
 bool make_tmap_out3(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t batch,
                     bool bf16) {
@@ -1362,70 +1279,6 @@ sq_status launch_gemm(const GemmArgs& a, cudaStream_t st) {
     e = launch_tiles<false>(L.ta, L.tb, L.ty, L.p, L.grid, L.tbn, bf16, st);
   }
   if (e != cudaSuccess) return fail(SQ_ERR_CUDA, "sq_gemm_w8a8: %s", cudaGetErrorString(e));
-  return SQ_OK;
-}
-
-namespace {
-// The grouped kernel: GROUP instances of the large-M kernel, one CTA per SM.
-template <bool BF16, int TBN, int EPI_W>
-cudaError_t launch_group(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
-                         const Params& p, int grid, cudaStream_t st) {
-  using C = TcCfg<TBN, 2, EPI_W>;
-  auto kern = gemm_w8a8_tc_kernel<BF16, TBN, false, 2, EPI_W, false, false, true>;
-  static std::once_flag once[64];
-  static cudaError_t attr_err[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
-  std::call_once(once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)C::SMEM_GROUP);
-  });
-  if (attr_err[dev] != cudaSuccess) return attr_err[dev];
-  return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM_GROUP, st, ta, tb, ty, p);
-}
-}  // namespace
-
-size_t gemm_grouped_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
-
-sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st) {
-  unsigned int* sw = status_word();
-  if (!sw) return fail(SQ_ERR_CUDA, "sq_gemm_w8a8_grouped: device status word unavailable");
-  constexpr int tbn = 256;
-  const bool bf16 = a.yt == SQ_BF16;
-  CUtensorMap ta, tb, ty;
-  memset(&ty, 0, sizeof ty);
-  if (!make_tmap(&ta, a.xq, (uint64_t)a.K, (uint64_t)a.R, BM) ||
-      !make_tmap3(&tb, a.wq, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, (uint32_t)tbn))
-    return fail(SQ_ERR_CUDA, "sq_gemm_w8a8_grouped: cuTensorMapEncodeTiled failed");
-  Params p{};
-  p.M = (int)a.R; p.N = (int)a.N; p.K = (int)a.K;
-  p.n_tiles = (int)((a.N + tbn - 1) / tbn);
-  p.group = GROUP_M;
-  p.nk = (int)((a.K + BK - 1) / BK);
-  p.act_scale = a.act_scale;
-  p.per_token = a.act_per_token;
-  p.w_scale = a.w_scale;
-  p.bias = a.bias;
-  p.y = a.y;
-  p.acc = a.acc_out;
-  p.y_elems = a.R * a.N;
-  p.status = sw;
-  p.offsets = a.offsets;
-  p.E = (int)a.E;
-  p.tma_store = (a.N % (bf16 ? 8 : 4)) == 0 &&
-                make_tmap_out(&ty, a.y, (uint64_t)a.N, (uint64_t)a.R, bf16);
-  const int64_t most = ((a.R + BM - 1) / BM + a.E) * p.n_tiles;  // tiles, whatever the offsets
-  int grid = sm_count();
-  if (grid > most) grid = (int)most;
-  cudaError_t e;
-  if (p.nk <= 4)
-    e = bf16 ? launch_group<true, 256, 12>(ta, tb, ty, p, grid, st)
-             : launch_group<false, 256, 12>(ta, tb, ty, p, grid, st);
-  else
-    e = bf16 ? launch_group<true, 256, 4>(ta, tb, ty, p, grid, st)
-             : launch_group<false, 256, 4>(ta, tb, ty, p, grid, st);
-  if (e != cudaSuccess) return fail(SQ_ERR_CUDA, "sq_gemm_w8a8_grouped: %s", cudaGetErrorString(e));
   return SQ_OK;
 }
 

@@ -1,0 +1,506 @@
+// grouped.cu -- the routed experts' INT8 GEMM: one weight matrix per group of
+// rows, the groups (offsets) known to the device alone.
+//
+//   acc[r,n] = sum_k xq[r,k] * wq[e,n,k],  offsets[e] <= r < offsets[e+1]
+//   y[r,n]   = (float)acc[r,n] * (as_r * w_scale[e,n]) (+ bias[e,n])
+//
+// Bound: an expert with few rows by the stream of its weights (HBM), one with
+// many by the tensor cores; they meet near 280 rows per expert.
+//
+// The operands are swapped: 256 of an expert's output channels fill the M
+// dimension of the MMA and up to 256 of its rows the N dimension, which takes
+// any multiple of 32.  So an expert with 300 rows computes 320 (two tiles of
+// 160), where 256-row tiles would compute 512: rows per expert are ragged,
+// channels are not.  The weights then stream through the A operand once per
+// 256 rows whatever the number of rows is.
+//
+// Persistent CTA pairs (tcgen05 cta_group::2, one pair per two SMs): each CTA
+// loads 128 channels of weights and half the tile's rows per 128-byte k-block
+// (16 KB + up to 16 KB), the even CTA issues the MMAs for both, each CTA
+// drains its 128 channels.  Two accumulators of 256 TMEM columns, so one
+// tile's epilogue runs under the next tile's main loop.  Warp 0 issues the
+// loads, warp 1 the MMAs, the others drain.  Every wait is bounded.
+//
+// The accumulator has channels along the TMEM lanes and rows along its
+// columns; the epilogue turns it round through shared memory.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <mutex>
+
+#include "launch.cuh"
+#include "sq_device.cuh"
+#include "sq_internal.h"
+#include "tc_ptx.cuh"
+#include "tmaps.h"
+
+namespace sq {
+
+namespace {
+
+constexpr int BK = 128;              // bytes of K per stage: one 128-byte swizzle row
+constexpr int UK = 32;               // K per tcgen05.mma kind::i8
+constexpr int CH = 128;              // channels per CTA
+constexpr int TILE_N = 2 * CH;       // channels per pair
+constexpr int TILE_R = 256;          // rows per tile, at most
+constexpr int STEP_R = 32;           // and their granularity (MMA N of a CTA pair)
+constexpr int W_BYTES = CH * BK;     // a stage's weights
+constexpr int X_BYTES = TILE_R / 2 * BK;  // and rows (at most)
+constexpr int STAGE = W_BYTES + X_BYTES;
+constexpr int BOXES = 4;             // row boxes of 16, 32, 64 and 128
+constexpr uint64_t kWaitNs = 4000000000ull;   // 4 s: far above any pipeline step
+constexpr uint64_t kDrainNs = 1000000000ull;  // waits for copies already in flight
+constexpr uint64_t kPairGraceNs = 2000000ull; // after a time-out: the peer's copies land
+constexpr uint32_t TMEM_COLS = 512;
+
+template <bool BF16, int EPI_W>
+struct Cfg {
+  static constexpr int THREADS = 64 + 32 * EPI_W;
+  static constexpr int EPI_BUF = BF16 ? 32 * 64 : 32 * 128;  // 32 rows x 32 channels
+  static constexpr int EPI_BYTES = EPI_W * 2 * EPI_BUF;      // two per warp
+  static constexpr int AS_BYTES = EPI_W * 32 * 4;            // the rows' steps, per warp
+  static constexpr int TABLE = 2 * (kMaxExperts + 1) * 4;
+  static constexpr int FIXED = 1024 + EPI_BYTES + AS_BYTES + 256 + TABLE;
+  static constexpr int STAGES = (227 * 1024 - FIXED) / STAGE;
+  static constexpr size_t SMEM = FIXED + (size_t)STAGES * STAGE;
+  static_assert(STAGES >= 4, "main-loop stages");
+};
+
+struct Params {
+  int R, N, E;
+  int n_tiles, nk;
+  int band;  // row tiles of a raster band
+  const int32_t* offsets;
+  const float* act_scale;
+  int per_token;
+  const float* w_scale;
+  const float* bias;
+  void* y;
+  int tma_store;
+  int32_t* acc;
+  unsigned int* status;
+};
+
+struct RowMaps {
+  CUtensorMap m[BOXES];
+};
+
+// One warp fills the CTA's table: off[e], the experts' first rows, and
+// tiles[e], the row tiles before expert e.  Offsets outside [0, R] or falling
+// ones are clamped to a rising sequence, so a bad table gives rows to the
+// wrong expert but touches nothing outside the arrays.
+__device__ __forceinline__ void group_table(const Params& p, int* off, int* tiles) {
+  const int lane = threadIdx.x & 31;
+  int top = 0, before = 0;
+  for (int e0 = 0; e0 <= p.E; e0 += 32) {
+    const int e = e0 + lane;
+    int v = e <= p.E ? min(max(__ldcg(p.offsets + e), 0), p.R) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, u);
+    }
+    v = max(v, top);
+    const int prev = __shfl_up_sync(0xffffffffu, v, 1);
+    // the rows between offsets e - 1 and e are expert e - 1's
+    const int n = e > 0 && e <= p.E ? (v - (lane ? prev : top) + TILE_R - 1) / TILE_R : 0;
+    int s = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (e <= p.E) {
+      off[e] = v;
+      tiles[e] = before + s;
+    }
+    top = __shfl_sync(0xffffffffu, v, 31);
+    before += __shfl_sync(0xffffffffu, s, 31);
+  }
+}
+
+// A tile: expert e, channels n0 .. n0 + 255, rows row0 .. row0 + rows - 1,
+// computed as mma_n rows.
+struct Tile {
+  int e, n0, row0, rows, mma_n;
+};
+
+// An expert's tiles in bands of p.band row tiles, each band sweeping every
+// channel with its row tiles innermost: the band's rows stay in L2 and a
+// channel tile's weights are read from HBM once per band.  Tiles ascend, so
+// the search for e goes on from the last tile's.  An expert's row tiles are
+// all of the same size but the last: its rows split evenly, up to a multiple
+// of 32.
+__device__ __forceinline__ void locate(const Params& p, const int* off, const int* tiles, int tile,
+                                       Tile& t) {
+  while (tile >= tiles[t.e + 1] * p.n_tiles) ++t.e;
+  const int m_tiles = tiles[t.e + 1] - tiles[t.e];
+  const int local = tile - tiles[t.e] * p.n_tiles;
+  const int per_band = p.band * p.n_tiles;
+  const int b = local / per_band, first = b * p.band;
+  const int bm = min(m_tiles - first, p.band), r = local - b * per_band;
+  const int mb = first + r % bm;
+  t.n0 = r / bm * TILE_N;
+  const int all = off[t.e + 1] - off[t.e];
+  const int per = ((all + m_tiles - 1) / m_tiles + STEP_R - 1) / STEP_R * STEP_R;
+  t.row0 = off[t.e] + mb * per;
+  t.rows = min(per, all - mb * per);
+  t.mma_n = (t.rows + STEP_R - 1) / STEP_R * STEP_R;
+}
+
+template <bool BF16, int EPI_W>
+__global__ void __launch_bounds__(Cfg<BF16, EPI_W>::THREADS, 1)
+grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ RowMaps tmX,
+               const __grid_constant__ CUtensorMap tmY, const Params p) {
+  using C = Cfg<BF16, EPI_W>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sW = smem;
+  uint8_t* sX = smem + STAGES * W_BYTES;
+  uint8_t* sEpi = smem + STAGES * STAGE;  // 1024-aligned
+  float* sAs = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::AS_BYTES);
+  // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], drain
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  int* tiles = off + kMaxExperts + 1;
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto full_bar = [&](int s) { return tc::smem_u32(bars + s); };
+  auto empty_bar = [&](int s) { return tc::smem_u32(bars + STAGES + s); };
+  auto tfull_bar = [&](int b) { return tc::smem_u32(bars + 2 * STAGES + b); };
+  auto tempty_bar = [&](int b) { return tc::smem_u32(bars + 2 * STAGES + 2 + b); };
+  const uint32_t drain_bar = tc::smem_u32(bars + 2 * STAGES + 4);
+  const int rank = (int)tc::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int unit0 = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      tc::mbar_init(full_bar(s), 1);
+      tc::mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(tfull_bar(b), 1);
+      tc::mbar_init(tempty_bar(b), 2 * EPI_W);  // the epilogue warps of both CTAs
+    }
+    tc::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    tc::mbar_fence_init();
+    tc::tma_prefetch_desc(&tmW);
+    for (int i = 0; i < BOXES; ++i) tc::tma_prefetch_desc(&tmX.m[i]);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc_pair(tc::smem_u32(tmem_slot), TMEM_COLS);
+    tc::tmem_relinquish_pair();
+  }
+  pdl_wait();  // nothing before this touches global memory
+  if (warp == 0) group_table(p, off, tiles);
+  tc::tc_fence_before();
+  tc::cluster_sync();  // the peer's barriers are initialised, this CTA's table is filled
+  tc::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int num_tiles = tiles[p.E] * p.n_tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (tc::elect_one()) {
+      uint32_t stage = 0, phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      Tile t{};
+      for (int tile = unit0; ok && tile < num_tiles; tile += units) {
+        locate(p, off, tiles, tile, t);
+        const int half = t.mma_n / 2;  // this CTA's rows of the MMA
+        const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        const CUtensorMap* mx = &tmX.m[box];
+        const uint32_t bytes = W_BYTES + (16u << box) * BK;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!tc::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, kWaitNs, p.status)) {
+            ok = false;
+            break;
+          }
+          // both CTAs' bytes complete on the even CTA's barrier, which alone
+          // expects them; rows past the tile are loaded and not stored
+          const uint32_t fb = tc::mapa_shared(full_bar(stage), 0);
+          if (leader) tc::mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+          tc::tma_load_3d_pair(tc::smem_u32(sW + stage * W_BYTES), &tmW, kb * BK, t.n0 + rank * CH,
+                               t.e, fb);
+          tc::tma_load_2d_pair(tc::smem_u32(sX + stage * X_BYTES), mx, kb * BK,
+                               t.row0 + rank * half, fb);
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        // let every load already issued land before the CTA exits; the odd
+        // CTA's complete on the even CTA's barriers, which it cannot wait on:
+        // a fixed grace period
+        int never = 0;
+        if (leader)
+          for (int s = 0; s < STAGES; ++s)
+            if (issued & (1u << s))
+              tc::mbar_wait(full_bar(s), (issued_par >> s) & 1u, &never, kDrainNs, p.status);
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kPairGraceNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (leader && tc::elect_one()) {
+      uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
+      bool ok = true;
+      Tile t{};
+      for (int tile = unit0; ok && tile < num_tiles; tile += units) {
+        locate(p, off, tiles, tile, t);
+        const uint32_t idesc = tc::idesc_i8(TILE_N, t.mma_n);
+        if (!tc::mbar_wait(tempty_bar(abuf), aphase ^ 1u, abort_flag, kWaitNs, p.status)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t d = tmem_base + abuf * TILE_R;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!tc::mbar_wait(full_bar(stage), phase, abort_flag, kWaitNs, p.status)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t w0 = tc::smem_u32(sW + stage * W_BYTES);
+          const uint32_t x0 = tc::smem_u32(sX + stage * X_BYTES);
+#pragma unroll
+          for (int k = 0; k < BK / UK; ++k)
+            tc::mma_i8_pair(d, tc::desc_k_sw128(w0 + k * UK), tc::desc_k_sw128(x0 + k * UK), idesc,
+                            (kb | k) != 0);
+          tc::mma_commit_pair(empty_bar(stage), 0x3);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc::mma_commit_pair(tfull_bar(abuf), 0x3);
+        abuf ^= 1u;
+        if (abuf == 0) aphase ^= 1u;
+      }
+      // every MMA issued so far must finish before TMEM is released
+      tc::mma_commit_pair(drain_bar, 0x1);
+      int never = 0;
+      tc::mbar_wait(drain_bar, 0, &never, kDrainNs, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;        // TMEM lanes 32*quarter .. +31: this warp's channels
+    const int chunk0 = (warp - 2) >> 2;  // first of its 32-row chunks
+    const uint64_t y_policy = tc::l2_policy_evict_first();  // y is not read back here
+    uint8_t* ebuf = sEpi + (warp - 2) * 2 * C::EPI_BUF;
+    float* as_w = sAs + (warp - 2) * 32;
+    uint32_t nstore = 0, abuf = 0, aphase = 0;
+    Tile t{};
+    for (int tile = unit0; tile < num_tiles; tile += units) {
+      locate(p, off, tiles, tile, t);
+      const int col0 = t.n0 + rank * CH + quarter * 32, n = col0 + lane;
+      const bool col_ok = n < p.N;
+      const size_t sn = (size_t)t.e * (size_t)p.N + (size_t)n;
+      const bool sn_ok = col_ok && in_bounds((int64_t)sn, 1, (int64_t)p.E * p.N, p.status);
+      const float ws = sn_ok ? __ldcg(p.w_scale + sn) : 0.0f;
+      const float bs = p.bias && sn_ok ? __ldcg(p.bias + sn) : 0.0f;
+      if (!tc::mbar_wait(tfull_bar(abuf), aphase, abort_flag, kWaitNs, p.status)) break;
+      tc::tc_fence_after();
+      const uint32_t taddr = tmem_base + abuf * TILE_R + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+      for (int c = chunk0 * 32; c < t.mma_n; c += 8 * EPI_W) {
+        const int row0 = t.row0 + c, valid = min(32, t.rows - c);
+        // the 32 rows' steps, one per lane, shared with the warp
+        const int ar = p.per_token ? row0 + min(lane, max(valid, 1) - 1) : 0;
+        const float as = __ldcg(p.act_scale + ar);
+        uint32_t r[32];
+        tc::tmem_ld32(taddr + c, r);
+        __syncwarp();  // the last chunk's steps are read
+        as_w[lane] = as;
+        __syncwarp();
+        tc::tmem_ld_wait();
+        float yv[32];
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 a4 = *reinterpret_cast<const float4*>(as_w + i);
+          const float av[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // (float)acc * (as * ws), then the bias: separate fp32 roundings
+            yv[i + k] = __fmul_rn(__int2float_rn((int)r[i + k]), __fmul_rn(av[k], ws));
+            if (p.bias) yv[i + k] = __fadd_rn(yv[i + k], bs);
+          }
+        }
+        const int64_t out = (int64_t)row0 * p.N + n;
+        if (p.acc && col_ok) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < valid && in_bounds(out + (int64_t)i * p.N, 1, (int64_t)p.R * p.N, p.status))
+              p.acc[out + (int64_t)i * p.N] = (int)r[i];
+        }
+        // a TMA store clips at the tensor's edge, not at the expert's: the
+        // last rows of an expert go by plain stores
+        if (!p.tma_store || valid < 32) {
+          if (col_ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < valid && in_bounds(out + (int64_t)i * p.N, 1, (int64_t)p.R * p.N, p.status)) {
+                if (BF16)
+                  reinterpret_cast<__nv_bfloat16*>(p.y)[out + (int64_t)i * p.N] =
+                      __float2bfloat16_rn(yv[i]);
+                else
+                  reinterpret_cast<float*>(p.y)[out + (int64_t)i * p.N] = yv[i];
+              }
+          }
+          continue;
+        }
+        uint8_t* buf = ebuf + (nstore & 1u) * C::EPI_BUF;
+        if (lane == 0) tc::bulk_wait_read<1>();  // the store before last has left `buf`
+        __syncwarp();
+        if constexpr (BF16) {
+          // Row i of 64 bytes holds the 32 channels.  Lanes 2l and 2l + 1
+          // exchange, so that each writes the pair of channels of one of two
+          // rows: 4-byte writes, 128 bytes a warp, no bank twice.  16-byte
+          // chunk k of row i lies at k ^ ((i >> 1) & 3), the 64-byte swizzle.
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float give = odd ? yv[i] : yv[i + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, yv[i + 1])
+                                         : __floats2bfloat162_rn(yv[i], got);
+            const int k = (lane >> 3) ^ ((i >> 1) & 3);
+            *reinterpret_cast<__nv_bfloat162*>(buf + (i + odd) * 64 + k * 16 +
+                                               ((lane >> 1) & 3) * 4) = v;
+          }
+        } else {
+          // Row i of 128 bytes: chunk k at k ^ (i & 7), the 128-byte swizzle.
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<float*>(buf + i * 128 + ((lane >> 2) ^ (i & 7)) * 16 +
+                                      (lane & 3) * 4) = yv[i];
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (col0 < p.N) tc::tma_store_2d_hint(&tmY, tc::smem_u32(buf), col0, row0, y_policy);
+          tc::bulk_commit();
+        }
+        ++nstore;
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tempty_bar(abuf), 0));
+      abuf ^= 1u;
+      if (abuf == 0) aphase ^= 1u;
+    }
+    if (lane == 0) tc::bulk_wait_all();  // staged outputs written before the CTA exits
+    __syncwarp();
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves while the other may still reach its barriers or
+  // shared memory
+  tc::cluster_sync();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// Row tiles per raster band: about 32 MB of rows, 4 to 16 tiles, as the plain
+// GEMM's CTA pairs take it.
+int band_tiles(int64_t K) {
+  const int64_t t = ((int64_t)32 << 20) / (TILE_R * K);
+  return t > 16 ? 16 : t < 4 ? 4 : (int)t;
+}
+
+// The number of pairs that can be resident at once is queried once per
+// device; a persistent launch never asks for more.
+template <bool BF16, int EPI_W>
+cudaError_t launch_t(const CUtensorMap& tw, const RowMaps& tx, const CUtensorMap& ty,
+                     const Params& p, int64_t most, cudaStream_t st) {
+  using C = Cfg<BF16, EPI_W>;
+  auto kern = grouped_kernel<BF16, EPI_W>;
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  static int max_pairs[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (err[dev] != cudaSuccess) return;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    err[dev] = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    max_pairs[dev] = n;
+  });
+  if (err[dev] != cudaSuccess) return err[dev];
+  if (max_pairs[dev] < 1) return cudaErrorInvalidConfiguration;
+  int64_t pairs = sm_count() / 2;
+  if (pairs > max_pairs[dev]) pairs = max_pairs[dev];
+  if (pairs > most) pairs = most;
+  return launch_pdl_cluster(kern, dim3(2 * (unsigned)pairs), dim3(C::THREADS), C::SMEM, st, 2u, tw,
+                            tx, ty, p);
+}
+
+}  // namespace
+
+size_t gemm_grouped_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st) {
+  const char* fn = "sq_gemm_w8a8_grouped";
+  unsigned int* sw = status_word();
+  if (!sw) return fail(SQ_ERR_CUDA, "%s: device status word unavailable", fn);
+  const bool bf16 = a.yt == SQ_BF16;
+  CUtensorMap tw, ty;
+  RowMaps tx;
+  memset(&ty, 0, sizeof ty);
+  bool ok = make_tmap3(&tw, a.wq, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, CH);
+  for (int i = 0; ok && i < BOXES; ++i)
+    ok = make_tmap(&tx.m[i], a.xq, (uint64_t)a.K, (uint64_t)a.R, 16u << i);
+  if (!ok) return fail(SQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+  Params p{};
+  p.R = (int)a.R; p.N = (int)a.N; p.E = (int)a.E;
+  p.n_tiles = (int)((a.N + TILE_N - 1) / TILE_N);
+  p.nk = (int)((a.K + BK - 1) / BK);
+  p.band = band_tiles(a.K);
+  p.offsets = a.offsets;
+  p.act_scale = a.act_scale;
+  p.per_token = a.act_per_token;
+  p.w_scale = a.w_scale;
+  p.bias = a.bias;
+  p.y = a.y;
+  p.acc = a.acc_out;
+  p.status = sw;
+  // TMA stores need 16-byte row pitches; other widths store directly
+  p.tma_store = (a.N % (bf16 ? 8 : 4)) == 0 &&
+                make_tmap_out(&ty, a.y, (uint64_t)a.N, (uint64_t)a.R, bf16, bf16 ? 64 : 128);
+  // tiles, whatever the offsets
+  const int64_t most = ((a.R + TILE_R - 1) / TILE_R + a.E) * p.n_tiles;
+  const cudaError_t e = bf16 ? launch_t<true, 4>(tw, tx, ty, p, most, st)
+                             : launch_t<false, 4>(tw, tx, ty, p, most, st);
+  if (e != cudaSuccess) return fail(SQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  return SQ_OK;
+}
+
+}  // namespace sq
