@@ -37,6 +37,9 @@
 #include "tc_ptx.cuh"
 #include "tmaps.h"
 
+#ifndef EPIW
+#define EPIW 8
+#endif
 namespace sq {
 
 namespace {
@@ -60,8 +63,10 @@ template <bool BF16, int EPI_W>
 struct Cfg {
   static constexpr int THREADS = 64 + 32 * EPI_W;
   static constexpr int EPI_BUF = BF16 ? 32 * 64 : 32 * 128;  // 32 rows x 32 channels
-  static constexpr int EPI_BYTES = EPI_W * 2 * EPI_BUF;      // two per warp
-  static constexpr int AS_BYTES = EPI_W * 32 * 4;            // the rows' steps, per warp
+  static constexpr int NB = EPI_W > 4 ? 1 : 2;               // buffers per warp
+  static constexpr int EPI_BYTES = EPI_W * NB * EPI_BUF;
+  static constexpr int MY_CHUNKS = TILE_R / 32 / (EPI_W / 4);  // 32-row chunks a warp drains
+  static constexpr int AS_BYTES = EPI_W * MY_CHUNKS * 32 * 4;  // their rows' steps
   static constexpr int TABLE = 2 * (kMaxExperts + 1) * 4;
   static constexpr int FIXED = 1024 + EPI_BYTES + AS_BYTES + 256 + TABLE;
   static constexpr int STAGES = (227 * 1024 - FIXED) / STAGE;
@@ -299,8 +304,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     const int quarter = warp & 3;        // TMEM lanes 32*quarter .. +31: this warp's channels
     const int chunk0 = (warp - 2) >> 2;  // first of its 32-row chunks
     const uint64_t y_policy = tc::l2_policy_evict_first();  // y is not read back here
-    uint8_t* ebuf = sEpi + (warp - 2) * 2 * C::EPI_BUF;
-    float* as_w = sAs + (warp - 2) * 32;
+    uint8_t* ebuf = sEpi + (warp - 2) * C::NB * C::EPI_BUF;
+    float* as_w = sAs + (warp - 2) * C::MY_CHUNKS * 32;
     uint32_t nstore = 0, abuf = 0, aphase = 0;
     Tile t{};
     for (int tile = unit0; tile < num_tiles; tile += units) {
@@ -311,25 +316,29 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       const bool sn_ok = col_ok && in_bounds((int64_t)sn, 1, (int64_t)p.E * p.N, p.status);
       const float ws = sn_ok ? __ldcg(p.w_scale + sn) : 0.0f;
       const float bs = p.bias && sn_ok ? __ldcg(p.bias + sn) : 0.0f;
+      // the steps of this warp's rows, one per lane and chunk, in shared memory
+      // before the accumulator is full
+      __syncwarp();  // the last tile's are read
+#pragma unroll
+      for (int i = 0; i < C::MY_CHUNKS; ++i) {
+        const int c = (chunk0 + i * (EPI_W / 4)) * 32 + lane;
+        as_w[i * 32 + lane] = __ldcg(p.act_scale + (p.per_token ? t.row0 + min(c, t.rows - 1) : 0));
+      }
+      __syncwarp();
       if (!tc::mbar_wait(tfull_bar(abuf), aphase, abort_flag, kWaitNs, p.status)) break;
       tc::tc_fence_after();
+      const float* as_c = as_w;
       const uint32_t taddr = tmem_base + abuf * TILE_R + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
-      for (int c = chunk0 * 32; c < t.mma_n; c += 8 * EPI_W) {
+      for (int c = chunk0 * 32; c < t.mma_n; c += 8 * EPI_W, as_c += 32) {
         const int row0 = t.row0 + c, valid = min(32, t.rows - c);
-        // the 32 rows' steps, one per lane, shared with the warp
-        const int ar = p.per_token ? row0 + min(lane, max(valid, 1) - 1) : 0;
-        const float as = __ldcg(p.act_scale + ar);
         uint32_t r[32];
         tc::tmem_ld32(taddr + c, r);
-        __syncwarp();  // the last chunk's steps are read
-        as_w[lane] = as;
-        __syncwarp();
         tc::tmem_ld_wait();
         float yv[32];
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          const float4 a4 = *reinterpret_cast<const float4*>(as_w + i);
+          const float4 a4 = *reinterpret_cast<const float4*>(as_c + i);
           const float av[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -361,8 +370,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           }
           continue;
         }
-        uint8_t* buf = ebuf + (nstore & 1u) * C::EPI_BUF;
-        if (lane == 0) tc::bulk_wait_read<1>();  // the store before last has left `buf`
+        uint8_t* buf = ebuf + nstore % C::NB * C::EPI_BUF;
+        if (lane == 0) tc::bulk_wait_read<C::NB - 1>();  // the store that last read `buf` is done
         __syncwarp();
         if constexpr (BF16) {
           // Row i of 64 bytes holds the 32 channels.  Lanes 2l and 2l + 1
@@ -497,8 +506,8 @@ sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st) {
                 make_tmap_out(&ty, a.y, (uint64_t)a.N, (uint64_t)a.R, bf16, bf16 ? 64 : 128);
   // tiles, whatever the offsets
   const int64_t most = ((a.R + TILE_R - 1) / TILE_R + a.E) * p.n_tiles;
-  const cudaError_t e = bf16 ? launch_t<true, 4>(tw, tx, ty, p, most, st)
-                             : launch_t<false, 4>(tw, tx, ty, p, most, st);
+  const cudaError_t e = bf16 ? launch_t<true, EPIW>(tw, tx, ty, p, most, st)
+                             : launch_t<false, EPIW>(tw, tx, ty, p, most, st);
   if (e != cudaSuccess) return fail(SQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   return SQ_OK;
 }
