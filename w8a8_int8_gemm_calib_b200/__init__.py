@@ -147,18 +147,29 @@ _ROW_TYPES = {torch.float32: SQ_F32, torch.bfloat16: SQ_BF16, torch.int8: SQ_I8}
 _ID_TYPES = {torch.int32: SQ_I32, torch.int64: SQ_I64}
 
 
-def _arg(t, what, dtype, numel):
-    """Pointer of a contiguous tensor of this type and size on the current
-    device (None: NULL)."""
+def _arg(t, what, dtype, numel, dev=None):
+    """Pointer of a contiguous tensor of this type and size on device `dev`,
+    the current one (None: NULL)."""
     if t is None:
         return None
     if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{what}: expected {numel} elements, got {t.numel()}")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != (torch.cuda.current_device() if dev is None else dev):
         raise ValueError(f"{what}: not on the current CUDA device")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _here(stream):
+    """The current device and the stream to use, as integers (short calls are
+    bound by the host: no Stream object is made)."""
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream(stream)
 
 
 def _scratch(workspace, need, what):
@@ -182,11 +193,12 @@ def sq_add_rms_smooth_quant_act(x, residual, h, xq, act_scale, gamma_s, eps=1e-5
     else:
         gran = SQ_ACT_PER_TOKEN_DYNAMIC if per_token else SQ_ACT_PER_TENSOR_STATIC
     steps = T if gran == SQ_ACT_PER_TOKEN_DYNAMIC else 1
+    dev, st = _here(stream)
     check(lib.sq_add_rms_smooth_quant_act(
-        _arg(x, "x", dt, T * K), _arg(residual, "residual", dt, T * K), _dt(x), T, K,
-        _arg(gamma_s, "gamma_s", torch.float32, K), eps, gran, _arg(h, "h", dt, T * K),
-        _arg(act_scale, "act_scale", torch.float32, steps), _arg(xq, "xq", torch.int8, T * K),
-        _arg(n_clipped, "n_clipped", torch.int64, 1), _stream(stream)),
+        _arg(x, "x", dt, T * K, dev), _arg(residual, "residual", dt, T * K, dev), _dt(x), T, K,
+        _arg(gamma_s, "gamma_s", torch.float32, K, dev), eps, gran, _arg(h, "h", dt, T * K, dev),
+        _arg(act_scale, "act_scale", torch.float32, steps, dev), _arg(xq, "xq", torch.int8, T * K, dev),
+        _arg(n_clipped, "n_clipped", torch.int64, 1, dev), st),
         "sq_add_rms_smooth_quant_act")
     return h, xq, act_scale
 
@@ -202,10 +214,11 @@ def sq_moe_sort(expert_ids, num_experts, offsets, pos, workspace=None, stream=No
     if expert_ids.dtype not in _ID_TYPES:
         raise TypeError(f"expert_ids: expected int32 or int64, got {expert_ids.dtype}")
     ws, nbytes = _scratch(workspace, sq_moe_sort_workspace_bytes(T, k, num_experts), "sq_moe_sort")
-    check(lib.sq_moe_sort(_arg(expert_ids, "expert_ids", expert_ids.dtype, T * k),
+    dev, st = _here(stream)
+    check(lib.sq_moe_sort(_arg(expert_ids, "expert_ids", expert_ids.dtype, T * k, dev),
                           _ID_TYPES[expert_ids.dtype], T, k, num_experts,
-                          _arg(offsets, "offsets", torch.int32, num_experts + 1),
-                          _arg(pos, "pos", torch.int32, T * k), ws, nbytes, _stream(stream)),
+                          _arg(offsets, "offsets", torch.int32, num_experts + 1, dev),
+                          _arg(pos, "pos", torch.int32, T * k, dev), ws, nbytes, st),
           "sq_moe_sort")
     return offsets, pos
 
@@ -217,11 +230,12 @@ def sq_moe_gather(x, pos, xs, scale=None, scale_s=None, stream=None):
     R, k = xs.shape[0], pos.shape[1]
     if x.dtype not in _ROW_TYPES:
         raise TypeError(f"x: expected int8, bfloat16 or float32, got {x.dtype}")
-    check(lib.sq_moe_gather(_arg(x, "x", x.dtype, T * K), _ROW_TYPES[x.dtype], T, K,
-                            _arg(scale, "scale", torch.float32, T),
-                            _arg(pos, "pos", torch.int32, T * k), k, R,
-                            _arg(xs, "xs", x.dtype, R * K),
-                            _arg(scale_s, "scale_s", torch.float32, R), _stream(stream)),
+    dev, st = _here(stream)
+    check(lib.sq_moe_gather(_arg(x, "x", x.dtype, T * K, dev), _ROW_TYPES[x.dtype], T, K,
+                            _arg(scale, "scale", torch.float32, T, dev),
+                            _arg(pos, "pos", torch.int32, T * k, dev), k, R,
+                            _arg(xs, "xs", x.dtype, R * K, dev),
+                            _arg(scale_s, "scale_s", torch.float32, R, dev), st),
           "sq_moe_gather")
     return xs, scale_s
 
@@ -232,11 +246,12 @@ def sq_moe_combine(z, pos, y, weights=None, residual=None, stream=None):
     the residual itself."""
     R, N = z.shape
     T, k = pos.shape
-    check(lib.sq_moe_combine(_arg(z, "z", z.dtype, R * N), _dt(z), R, N,
-                             _arg(pos, "pos", torch.int32, T * k),
-                             _arg(weights, "weights", torch.float32, T * k), T, k,
-                             _arg(residual, "residual", z.dtype, T * N),
-                             _arg(y, "y", z.dtype, T * N), _stream(stream)), "sq_moe_combine")
+    dev, st = _here(stream)
+    check(lib.sq_moe_combine(_arg(z, "z", z.dtype, R * N, dev), _dt(z), R, N,
+                             _arg(pos, "pos", torch.int32, T * k, dev),
+                             _arg(weights, "weights", torch.float32, T * k, dev), T, k,
+                             _arg(residual, "residual", z.dtype, T * N, dev),
+                             _arg(y, "y", z.dtype, T * N, dev), st), "sq_moe_combine")
     return y
 
 
@@ -249,13 +264,14 @@ def sq_moe_combine_grad(dy, pos, z=None, weights=None, dz=None, dweights=None, s
     R = 0 if rows is None else rows.shape[0]
     if dweights is not None and z is None:
         raise ValueError("dweights needs z")
-    check(lib.sq_moe_combine_grad(_arg(dy, "dy", dy.dtype, T * N), _dt(dy), T, N,
-                                  _arg(pos, "pos", torch.int32, T * k),
-                                  _arg(weights, "weights", torch.float32, T * k), k,
-                                  _arg(z, "z", dy.dtype, R * N), R,
-                                  _arg(dz, "dz", dy.dtype, R * N),
-                                  _arg(dweights, "dweights", torch.float32, T * k),
-                                  _stream(stream)), "sq_moe_combine_grad")
+    dev, st = _here(stream)
+    check(lib.sq_moe_combine_grad(_arg(dy, "dy", dy.dtype, T * N, dev), _dt(dy), T, N,
+                                  _arg(pos, "pos", torch.int32, T * k, dev),
+                                  _arg(weights, "weights", torch.float32, T * k, dev), k,
+                                  _arg(z, "z", dy.dtype, R * N, dev), R,
+                                  _arg(dz, "dz", dy.dtype, R * N, dev),
+                                  _arg(dweights, "dweights", torch.float32, T * k, dev),
+                                  st), "sq_moe_combine_grad")
     return dz, dweights
 
 
@@ -364,15 +380,16 @@ def sq_gemm_w8a8_grouped(xq, wq, offsets, act_scale, w_scale, y, per_token=True,
     E, N, _ = wq.shape
     ws, nbytes = _scratch(workspace, sq_gemm_w8a8_grouped_workspace_bytes(R, N, K, E),
                           "sq_gemm_w8a8_grouped")
-    check(lib.sq_gemm_w8a8_grouped(_arg(xq, "xq", torch.int8, R * K),
-                                   _arg(wq, "wq", torch.int8, E * N * K),
-                                   _arg(offsets, "offsets", torch.int32, E + 1), R, N, K, E,
-                                   _arg(act_scale, "act_scale", torch.float32, R if per_token else 1),
-                                   int(per_token), _arg(w_scale, "w_scale", torch.float32, E * N),
-                                   _arg(bias, "bias", torch.float32, E * N),
-                                   _arg(y, "y", y.dtype, R * N), _dt(y),
-                                   _arg(acc_out, "acc_out", torch.int32, R * N), ws, nbytes,
-                                   _stream(stream)), "sq_gemm_w8a8_grouped")
+    dev, st = _here(stream)
+    check(lib.sq_gemm_w8a8_grouped(_arg(xq, "xq", torch.int8, R * K, dev),
+                                   _arg(wq, "wq", torch.int8, E * N * K, dev),
+                                   _arg(offsets, "offsets", torch.int32, E + 1, dev), R, N, K, E,
+                                   _arg(act_scale, "act_scale", torch.float32, R if per_token else 1, dev),
+                                   int(per_token), _arg(w_scale, "w_scale", torch.float32, E * N, dev),
+                                   _arg(bias, "bias", torch.float32, E * N, dev),
+                                   _arg(y, "y", y.dtype, R * N, dev), _dt(y),
+                                   _arg(acc_out, "acc_out", torch.int32, R * N, dev), ws, nbytes,
+                                   st), "sq_gemm_w8a8_grouped")
     return y
 
 

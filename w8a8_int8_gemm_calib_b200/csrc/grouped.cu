@@ -354,6 +354,33 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             if (i < valid && in_bounds(out + (int64_t)i * p.N, 1, (int64_t)p.R * p.N, p.status))
               p.acc[out + (int64_t)i * p.N] = (int)r[i];
         }
+#ifdef DIRECT
+        if constexpr (BF16) {
+          __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.y);
+          if ((p.N & 1) == 0) {
+            const bool odd = lane & 1;
+            const int64_t o2 = out - odd + (odd ? p.N : 0);  // the pair's first channel, this lane's row
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float give = odd ? yv[i] : yv[i + 1];
+              const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+              const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, yv[i + 1])
+                                           : __floats2bfloat162_rn(yv[i], got);
+              if (i + odd < valid && col_ok)
+                __stcs(reinterpret_cast<unsigned int*>(y + o2 + (int64_t)i * p.N), *reinterpret_cast<const unsigned int*>(&v));
+            }
+          } else if (col_ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < valid) y[out + (int64_t)i * p.N] = __float2bfloat16_rn(yv[i]);
+          }
+        } else if (col_ok) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < valid) __stcs(reinterpret_cast<float*>(p.y) + out + (int64_t)i * p.N, yv[i]);
+        }
+        continue;
+#endif
         // a TMA store clips at the tensor's edge, not at the expert's: the
         // last rows of an expert go by plain stores
         if (!p.tma_store || valid < 32) {

@@ -32,14 +32,18 @@ namespace {
 // counts of the parts and runs before it, plus its rank in the run, which
 // the warp finds 32 assignments at a time by matching equal experts.  Counts
 // are integers, so the order the atomics run in changes nothing.
-constexpr int kSortWarps = 8;
-constexpr int kSortThreads = 32 * kSortWarps;
-constexpr int kSortSteps = 8;  // least steps of 32 per warp before blocks are added
+//
+// W warps per block: 32 when there is work for them and their counts fit
+// (E <= 256), else 8.  A warp takes 64 / W steps of 32 assignments at once,
+// so one block holds 2048 either way.
+constexpr int kSortItems = 2048;
+constexpr int kSortWide = 256;   // experts
+constexpr int kSortFew = 512;    // assignments that 8 warps place as fast
 
 struct SortArgs {
   const void* ids;
   int ids64;
-  int64_t n, part;  // assignments, and those of a block (a multiple of kSortThreads)
+  int64_t n, part;  // assignments, and those of a block (a multiple of 32 W)
   int E, blocks;
   int32_t* offsets;
   int32_t* pos;
@@ -55,73 +59,117 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i) {
   return id >= 0 && id < a.E ? (int)id : a.E;
 }
 
-// cnt[warp][e] = the warp's assignments to e
-__device__ __forceinline__ void count_runs(const SortArgs& a, int* cnt, int64_t run0, int64_t run1) {
-  for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) cnt[i] = 0;
+// A run is counted S = 64 / W steps at a time, their loads in flight
+// together; a warp with no more than that keeps its experts for placing.
+struct Run {
+  int64_t begin, end;
+};
+template <int W>
+__device__ __forceinline__ Run run_of(const SortArgs& a) {
+  const int64_t run = a.part / W;
+  Run r;
+  r.begin = blockIdx.x * a.part + (threadIdx.x >> 5) * run;
+  r.end = r.begin + run < a.n ? r.begin + run : a.n;
+  return r;
+}
+template <int S>
+__device__ __forceinline__ void load_steps(const SortArgs& a, int64_t i0, int64_t end,
+                                           int (&e8)[S]) {
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int64_t i = i0 + s * 32 + (threadIdx.x & 31);
+    e8[s] = i < end ? expert_of(a, i) : a.E;
+  }
+}
+// cnt[warp][e] = the warp's assignments to e; rows of E + 1, so that a warp
+// reading one expert's counts of 32 warps hits 32 banks
+template <int W>
+__device__ __forceinline__ void count_runs(const SortArgs& a, int* cnt, const Run& run,
+                                           int (&e8)[64 / W]) {
+  load_steps(a, run.begin, run.end, e8);
+  for (int i = threadIdx.x; i < W * (a.E + 1); i += 32 * W) cnt[i] = 0;
   __syncthreads();
-  int* mine = cnt + (threadIdx.x >> 5) * a.E;
-  for (int64_t i = run0 + (threadIdx.x & 31); i < run1; i += 32) {
-    const int e = expert_of(a, i);
-    if (e < a.E) atomicAdd(mine + e, 1);
+  int* mine = cnt + (threadIdx.x >> 5) * (a.E + 1);
+  for (int64_t i0 = run.begin;;) {
+#pragma unroll
+    for (int s = 0; s < 64 / W; ++s)
+      if (e8[s] < a.E) atomicAdd(mine + e8[s], 1);
+    i0 += 32 * (64 / W);
+    if (i0 >= run.end) break;
+    load_steps(a, i0, run.end, e8);
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ void run_of(const SortArgs& a, int64_t& run0, int64_t& run1) {
-  const int64_t run = a.part / kSortWarps;
-  run0 = blockIdx.x * a.part + (threadIdx.x >> 5) * run;
-  run1 = run0 + run;
-  if (run1 > a.n) run1 = a.n;
-}
-
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+template <int W>
+__global__ void __launch_bounds__(32 * W) sort_count_kernel(const SortArgs a) {
   extern __shared__ int cnt[];
   pdl_launch_dependents();
   pdl_wait();
-  int64_t run0, run1;
-  run_of(a, run0, run1);
-  count_runs(a, cnt, run0, run1);
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+  int e8[64 / W];
+  count_runs<W>(a, cnt, run_of<W>(a), e8);
+  for (int e = threadIdx.x; e < a.E; e += 32 * W) {
     int s = 0;
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) s += cnt[w * a.E + e];
+    for (int w = 0; w < W; ++w) s += cnt[w * (a.E + 1) + e];
     const int64_t o = (int64_t)blockIdx.x * a.E + e;
     if (in_bounds(o, 1, (int64_t)a.blocks * a.E, a.status)) a.counts[o] = s;
   }
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs a) {
-  extern __shared__ int cnt[];        // [warps][E], then the experts' totals [E]
-  int* total = cnt + kSortWarps * a.E;
-  __shared__ int warp_sum[kSortWarps];
+template <int W>
+__global__ void __launch_bounds__(32 * W) sort_place_kernel(const SortArgs a) {
+  constexpr int kSortThreads = 32 * W, S = 64 / W;
+  // [warps][E + 1], the experts' totals [E] and their assignments in the
+  // blocks before this one [E]
+  extern __shared__ int cnt[];
+  int* total = cnt + W * (a.E + 1);
+  int* before = total + a.E;
+  __shared__ int warp_sum[W];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t run0, run1;
-  run_of(a, run0, run1);
-  count_runs(a, cnt, run0, run1);
-  // totals over the call, and each run's start within its expert
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
-    int before = 0, all = 0;
-    if (a.blocks > 1) {
-#pragma unroll 8
-      for (int b = 0; b < a.blocks; ++b) {
-        const int64_t o = (int64_t)b * a.E + e;
-        const int v = in_bounds(o, 1, (int64_t)a.blocks * a.E, a.status) ? __ldcg(a.counts + o) : 0;
-        all += v;
-        before += b < (int)blockIdx.x ? v : 0;
+  for (int e = threadIdx.x; e < 2 * a.E; e += kSortThreads) total[e] = 0;
+  const Run run = run_of<W>(a);
+  int e8[S];
+  count_runs<W>(a, cnt, run, e8);
+  const bool kept = run.end - run.begin <= 32 * S;
+  if (a.blocks > 1) {
+    // every block's counts, summed by all threads, eight loads in flight
+    const unsigned all = (unsigned)a.blocks * a.E, mine = blockIdx.x * a.E;
+    for (unsigned o0 = threadIdx.x; o0 < all; o0 += 8 * kSortThreads) {
+      int v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const unsigned o = o0 + u * kSortThreads;
+        v[u] = o < all && in_bounds(o, 1, all, a.status) ? __ldcg(a.counts + o) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const unsigned o = o0 + u * kSortThreads, e = o % (unsigned)a.E;
+        if (v[u]) {
+          atomicAdd(total + e, v[u]);
+          if (o < mine) atomicAdd(before + e, v[u]);
+        }
       }
     }
+    __syncthreads();
+  }
+  // the runs' starts within the block, a warp per expert
+  for (int e = warp; e < a.E; e += W) {
+    const int v = lane < W ? cnt[lane * (a.E + 1) + e] : 0;
+    int s = v;
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int v = cnt[w * a.E + e];
-      cnt[w * a.E + e] = before;
-      before += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
     }
-    total[e] = a.blocks > 1 ? all : before;
+    if (lane < W) cnt[lane * (a.E + 1) + e] = s - v;
+    if (a.blocks == 1 && lane == 31) total[e] = s;
   }
   __syncthreads();
-  // exclusive sums of the totals: the offsets, added to every run's start
+  // exclusive sums of the totals are the offsets; with the blocks before
+  // this one they replace `before`
   int carry = 0;
   for (int e0 = 0; e0 < a.E; e0 += kSortThreads) {
     const int e = e0 + threadIdx.x;
@@ -134,44 +182,63 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
     }
     if (lane == 31) warp_sum[warp] = s;
     __syncthreads();
-    int below = carry;
-    for (int w = 0; w < kSortWarps; ++w) {
-      if (w < warp) below += warp_sum[w];
-      carry += warp_sum[w];
-    }
-    const int off = below + s - v;
-    if (e < a.E) {
+    // the warps' sums, one per lane
+    int ws = lane < W ? warp_sum[lane] : 0;
 #pragma unroll
-      for (int w = 0; w < kSortWarps; ++w) cnt[w * a.E + e] += off;
-      if (blockIdx.x == 0) a.offsets[e] = off;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, ws, o);
+      if (lane >= o) ws += u;
+    }
+    const int upto = __shfl_sync(0xffffffffu, ws, warp > 0 ? warp - 1 : 0);
+    const int at = carry + (warp > 0 ? upto : 0) + s - v;
+    carry += __shfl_sync(0xffffffffu, ws, 31);
+    if (e < a.E) {
+      if (blockIdx.x == 0) a.offsets[e] = at;
+      before[e] += at;
     }
     __syncthreads();
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = carry;
   // places, 32 assignments at a time in order
-  int* mine = cnt + warp * a.E;
-  for (int64_t i0 = run0; i0 < run1; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int e = i < run1 ? expert_of(a, i) : a.E;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    int at = -1;
-    if (e < a.E) at = mine[e] + rank;
-    __syncwarp();
-    if (e < a.E && rank == 0) mine[e] += __popc(same);
-    __syncwarp();
-    if (i < run1 && in_bounds(i, 1, a.n, a.status)) a.pos[i] = at;
+  int* next = cnt + warp * (a.E + 1);
+  for (int64_t i0 = run.begin; i0 < run.end; i0 += 32 * S) {
+    if (!kept) load_steps(a, i0, run.end, e8);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int64_t i = i0 + s * 32 + lane;
+      const int e = e8[s];
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      int at = -1;
+      if (e < a.E) at = before[e] + next[e] + rank;
+      __syncwarp();
+      if (e < a.E && rank == 0) next[e] += __popc(same);
+      __syncwarp();
+      if (i < run.end && in_bounds(i, 1, a.n, a.status)) a.pos[i] = at;
+    }
   }
 }
 
-// Blocks: one up to kSortSteps steps of a warp (2048 assignments), then as
-// many as that leaves work for, one per SM at most (every block sums the
-// counts of all).
+// Blocks: one up to 2048 assignments, then as many as that leaves work for,
+// one per SM at most (every block sums the counts of all).
 int sort_blocks(int64_t n) {
-  const int64_t least = (int64_t)kSortThreads * kSortSteps;
-  const int64_t b = (n + least - 1) / least;
+  const int64_t b = (n + kSortItems - 1) / kSortItems;
   const int64_t most = sm_count();
   return (int)(b < 1 ? 1 : b > most ? most : b);
+}
+
+template <int W>
+cudaError_t launch_sort_t(SortArgs a, cudaStream_t st) {
+  const int64_t part = (a.n + a.blocks - 1) / a.blocks;
+  a.part = (part + 32 * W - 1) / (32 * W) * (32 * W);
+  const size_t smem = (size_t)W * (a.E + 1) * sizeof(int);
+  if (a.blocks > 1) {
+    const cudaError_t e =
+        launch_pdl(sort_count_kernel<W>, dim3(a.blocks), dim3(32 * W), smem, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(sort_place_kernel<W>, dim3(a.blocks), dim3(32 * W),
+                    smem + 2 * (size_t)a.E * sizeof(int), st, a);
 }
 
 // ====================================================================== rows
@@ -283,8 +350,9 @@ __global__ void __launch_bounds__(kRowThreads, kCombineBlocks) combine_kernel(co
   int row = -1;
   float wt = 1.0f;
   auto fetch = [&](int64_t t, int k0) {
-    row = (int)place(a, t, t < a.T ? k0 + lane : a.top_k);
-    if (row >= 0 && a.w) wt = __ldcg(a.w + t * a.top_k + k0 + lane);
+    const int k = t < a.T ? k0 + lane : a.top_k;
+    if (a.w && k < a.top_k) wt = __ldcg(a.w + t * a.top_k + k);
+    row = (int)place(a, t, k);
   };
   fetch(blockIdx.x, 0);
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -372,9 +440,9 @@ __global__ void __launch_bounds__(kRowThreads, kGradBlocks) combine_grad_kernel(
   float wt = 1.0f;
   // place and weight of assignment k0 + (lane mod 8), one batch ahead
   auto fetch = [&](int64_t t, int k0) {
-    const int k = k0 + (lane & (kBatch - 1));
-    row = (int)place(a, t, t < a.T ? k : a.top_k);
-    if (row >= 0 && a.w) wt = __ldcg(a.w + t * a.top_k + k);
+    const int k = t < a.T ? k0 + (lane & (kBatch - 1)) : a.top_k;
+    if (a.w && k < a.top_k) wt = __ldcg(a.w + t * a.top_k + k);
+    row = (int)place(a, t, k);
   };
   fetch(blockIdx.x, 0);
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -472,20 +540,11 @@ cudaError_t launch_moe_sort(const void* ids, bool ids64, int64_t n, int E, int32
   SortArgs a{};
   a.ids = ids; a.ids64 = ids64; a.n = n; a.E = E;
   a.blocks = sort_blocks(n);
-  const int64_t part = (n + a.blocks - 1) / a.blocks;
-  a.part = (part + kSortThreads - 1) / kSortThreads * kSortThreads;
   a.offsets = offsets; a.pos = pos;
   a.counts = static_cast<int32_t*>(workspace);
   a.status = status_word();
   if (!a.status) return cudaErrorInvalidDevice;
-  const size_t smem = (size_t)kSortWarps * E * sizeof(int);
-  if (a.blocks > 1) {
-    const cudaError_t e = launch_pdl(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads), smem,
-                                     st, a);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(sort_place_kernel, dim3(a.blocks), dim3(kSortThreads),
-                    smem + (size_t)E * sizeof(int), st, a);
+  return E <= kSortWide && n > kSortFew ? launch_sort_t<32>(a, st) : launch_sort_t<8>(a, st);
 }
 
 cudaError_t launch_moe_gather(MoeArgs a, size_t elem, cudaStream_t st) {
