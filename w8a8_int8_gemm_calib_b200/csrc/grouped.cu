@@ -301,8 +301,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
+    // A warp drains 32 channels x 32 rows at a time with two 16x256b loads: in
+    // fragment m (channels 16 m ..), lane l holds channels cl and cl + 8, cl =
+    // l / 4, of rows 2 (l % 4) and the next, for each of four groups of 8
+    // rows.  Transposing 8x8 stores of bf16 pairs (stmatrix.trans) then write
+    // whole 16-byte pieces of output rows.
     const int quarter = warp & 3;        // TMEM lanes 32*quarter .. +31: this warp's channels
     const int chunk0 = (warp - 2) >> 2;  // first of its 32-row chunks
+    const int cl = lane >> 2, rl = 2 * (lane & 3);
     const uint64_t y_policy = tc::l2_policy_evict_first();  // y is not read back here
     uint8_t* ebuf = sEpi + (warp - 2) * C::NB * C::EPI_BUF;
     float* as_w = sAs + (warp - 2) * C::MY_CHUNKS * 32;
@@ -310,12 +316,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     Tile t{};
     for (int tile = unit0; tile < num_tiles; tile += units) {
       locate(p, off, tiles, tile, t);
-      const int col0 = t.n0 + rank * CH + quarter * 32, n = col0 + lane;
-      const bool col_ok = n < p.N;
-      const size_t sn = (size_t)t.e * (size_t)p.N + (size_t)n;
-      const bool sn_ok = col_ok && in_bounds((int64_t)sn, 1, (int64_t)p.E * p.N, p.status);
-      const float ws = sn_ok ? __ldcg(p.w_scale + sn) : 0.0f;
-      const float bs = p.bias && sn_ok ? __ldcg(p.bias + sn) : 0.0f;
+      const int col0 = t.n0 + rank * CH + quarter * 32;
+      float ws[4], bs[4];  // channels col0 + cl + 8 i
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = col0 + cl + 8 * i;
+        const int64_t sn = (int64_t)t.e * p.N + n;
+        const bool ok = n < p.N && in_bounds(sn, 1, (int64_t)p.E * p.N, p.status);
+        ws[i] = ok ? __ldcg(p.w_scale + sn) : 0.0f;
+        bs[i] = ok && p.bias ? __ldcg(p.bias + sn) : 0.0f;
+      }
       // the steps of this warp's rows, one per lane and chunk, in shared memory
       // before the accumulator is full
       __syncwarp();  // the last tile's are read
@@ -332,104 +342,95 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 #pragma unroll 1
       for (int c = chunk0 * 32; c < t.mma_n; c += 8 * EPI_W, as_c += 32) {
         const int row0 = t.row0 + c, valid = min(32, t.rows - c);
-        uint32_t r[32];
-        tc::tmem_ld32(taddr + c, r);
+        // r[m][4 g + ...]: channels 16 m + {cl, cl, cl + 8, cl + 8}, rows 8 g +
+        // {rl, rl + 1, rl, rl + 1}
+        uint32_t r[2][16];
+        tc::tmem_ld_16x256b_x4(taddr + c, r[0]);
+        tc::tmem_ld_16x256b_x4(taddr + c + (16u << 16), r[1]);
         tc::tmem_ld_wait();
-        float yv[32];
+        if (p.acc) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 a4 = *reinterpret_cast<const float4*>(as_c + i);
-          const float av[4] = {a4.x, a4.y, a4.z, a4.w};
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // (float)acc * (as * ws), then the bias: separate fp32 roundings
-            yv[i + k] = __fmul_rn(__int2float_rn((int)r[i + k]), __fmul_rn(av[k], ws));
-            if (p.bias) yv[i + k] = __fadd_rn(yv[i + k], bs);
-          }
-        }
-        const int64_t out = (int64_t)row0 * p.N + n;
-        if (p.acc && col_ok) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < valid && in_bounds(out + (int64_t)i * p.N, 1, (int64_t)p.R * p.N, p.status))
-              p.acc[out + (int64_t)i * p.N] = (int)r[i];
-        }
-#ifdef DIRECT
-        if constexpr (BF16) {
-          __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.y);
-          if ((p.N & 1) == 0) {
-            const bool odd = lane & 1;
-            const int64_t o2 = out - odd + (odd ? p.N : 0);  // the pair's first channel, this lane's row
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float give = odd ? yv[i] : yv[i + 1];
-              const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-              const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, yv[i + 1])
-                                           : __floats2bfloat162_rn(yv[i], got);
-              if (i + odd < valid && col_ok)
-                __stcs(reinterpret_cast<unsigned int*>(y + o2 + (int64_t)i * p.N), *reinterpret_cast<const unsigned int*>(&v));
+            for (int i = 0; i < 16; ++i) {
+              const int row = 8 * (i >> 2) + rl + (i & 1);
+              const int n = col0 + 16 * m + cl + 8 * ((i >> 1) & 1);
+              const int64_t o = (int64_t)(row0 + row) * p.N + n;
+              if (row < valid && n < p.N && in_bounds(o, 1, (int64_t)p.R * p.N, p.status))
+                p.acc[o] = (int)r[m][i];
             }
-          } else if (col_ok) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < valid) y[out + (int64_t)i * p.N] = __float2bfloat16_rn(yv[i]);
-          }
-        } else if (col_ok) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < valid) __stcs(reinterpret_cast<float*>(p.y) + out + (int64_t)i * p.N, yv[i]);
-        }
-        continue;
-#endif
-        // a TMA store clips at the tensor's edge, not at the expert's: the
-        // last rows of an expert go by plain stores
-        if (!p.tma_store || valid < 32) {
-          if (col_ok) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < valid && in_bounds(out + (int64_t)i * p.N, 1, (int64_t)p.R * p.N, p.status)) {
-                if (BF16)
-                  reinterpret_cast<__nv_bfloat16*>(p.y)[out + (int64_t)i * p.N] =
-                      __float2bfloat16_rn(yv[i]);
-                else
-                  reinterpret_cast<float*>(p.y)[out + (int64_t)i * p.N] = yv[i];
-              }
-          }
-          continue;
         }
         uint8_t* buf = ebuf + nstore % C::NB * C::EPI_BUF;
         if (lane == 0) tc::bulk_wait_read<C::NB - 1>();  // the store that last read `buf` is done
         __syncwarp();
-        if constexpr (BF16) {
-          // Row i of 64 bytes holds the 32 channels.  Lanes 2l and 2l + 1
-          // exchange, so that each writes the pair of channels of one of two
-          // rows: 4-byte writes, 128 bytes a warp, no bank twice.  16-byte
-          // chunk k of row i lies at k ^ ((i >> 1) & 3), the 64-byte swizzle.
-          const bool odd = lane & 1;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float give = odd ? yv[i] : yv[i + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, yv[i + 1])
-                                         : __floats2bfloat162_rn(yv[i], got);
-            const int k = (lane >> 3) ^ ((i >> 1) & 3);
-            *reinterpret_cast<__nv_bfloat162*>(buf + (i + odd) * 64 + k * 16 +
-                                               ((lane >> 1) & 3) * 4) = v;
+        for (int g = 0; g < 4; ++g) {
+          const float2 as = *reinterpret_cast<const float2*>(as_c + 8 * g + rl);
+          float v[2][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // (float)acc * (as * ws), then the bias: separate fp32 roundings
+              const int w = 2 * m + (i >> 1);
+              const float y = __fmul_rn(__int2float_rn((int)r[m][4 * g + i]),
+                                        __fmul_rn(i & 1 ? as.y : as.x, ws[w]));
+              v[m][i] = p.bias ? __fadd_rn(y, bs[w]) : y;
+            }
+          if constexpr (BF16) {
+            // Output rows 8 g .. 8 g + 7 of 64 bytes: piece k (8 channels) of
+            // row i at k ^ ((i >> 1) & 3), the 64-byte swizzle.  Lane l gives
+            // the address of row l % 8 of piece l / 8.
+            uint32_t q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(v[k >> 1][2 * (k & 1)], v[k >> 1][2 * (k & 1) + 1]);
+              q[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            const int i = 8 * g + (lane & 7), k = (lane >> 3) ^ ((i >> 1) & 3);
+            tc::stmatrix_x4_trans(tc::smem_u32(buf + i * 64 + k * 16), q);
+          } else {
+            // Output rows of 128 bytes: 16-byte piece k of row i at k ^ (i & 7),
+            // the 128-byte swizzle; 8 lanes write 32 bytes of one row, the four
+            // rows of a warp's write differ in their banks.
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = 8 * g + rl + (e & 1), ch = 16 * m + cl + 8 * (e >> 1);
+                *reinterpret_cast<float*>(buf + i * 128 + ((ch >> 2) ^ (i & 7)) * 16 + (ch & 3) * 4) =
+                    v[m][e];
+              }
           }
-        } else {
-          // Row i of 128 bytes: chunk k at k ^ (i & 7), the 128-byte swizzle.
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            *reinterpret_cast<float*>(buf + i * 128 + ((lane >> 2) ^ (i & 7)) * 16 +
-                                      (lane & 3) * 4) = yv[i];
         }
-        tc::fence_proxy_async_smem();
+        if (p.tma_store && valid == 32) {
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (col0 < p.N) tc::tma_store_2d_hint(&tmY, tc::smem_u32(buf), col0, row0, y_policy);
+            tc::bulk_commit();
+          }
+          ++nstore;
+          continue;
+        }
+        // A TMA store clips at the tensor's edge, not at the expert's, and
+        // needs 16-byte row pitches: otherwise the rows are written from the
+        // buffer, a row per step.
         __syncwarp();
-        if (lane == 0) {
-          if (col0 < p.N) tc::tma_store_2d_hint(&tmY, tc::smem_u32(buf), col0, row0, y_policy);
-          tc::bulk_commit();
+        const int n = col0 + lane;
+        if (n < p.N) {
+          for (int i = 0; i < valid; ++i) {
+            const int64_t o = (int64_t)(row0 + i) * p.N + n;
+            if (!in_bounds(o, 1, (int64_t)p.R * p.N, p.status)) continue;
+            if (BF16)
+              reinterpret_cast<uint16_t*>(p.y)[o] = *reinterpret_cast<const uint16_t*>(
+                  buf + i * 64 + ((lane >> 3) ^ ((i >> 1) & 3)) * 16 + (lane & 7) * 2);
+            else
+              reinterpret_cast<float*>(p.y)[o] = *reinterpret_cast<const float*>(
+                  buf + i * 128 + ((lane >> 2) ^ (i & 7)) * 16 + (lane & 3) * 4);
+          }
         }
-        ++nstore;
+        __syncwarp();  // read before the next chunk overwrites it
       }
       tc::tc_fence_before();
       __syncwarp();

@@ -255,6 +255,26 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+// 16 lanes x 32 columns in fragments: register 4 g + i of lane l holds TMEM
+// lane l / 4 (i < 2) or l / 4 + 8, column 8 g + 2 (l % 4) + i % 2.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Four 8x8 matrices of 16-bit elements, each stored transposed: lane l holds
+// row l / 4, columns 2 (l % 4) and the next, of matrix k in q[k]; lane 8 k + j
+// gives the address of the 16 bytes that receive column j of matrix k.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&q)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
