@@ -313,28 +313,42 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint8_t* ebuf = sEpi + (warp - 2) * C::NB * C::EPI_BUF;
     float* as_w = sAs + (warp - 2) * C::MY_CHUNKS * 32;
     uint32_t nstore = 0, abuf = 0, aphase = 0;
-    Tile t{};
-    for (int tile = unit0; tile < num_tiles; tile += units) {
-      locate(p, off, tiles, tile, t);
-      const int col0 = t.n0 + rank * CH + quarter * 32;
-      float ws[4], bs[4];  // channels col0 + cl + 8 i
+    // A tile's place, its channels' steps and biases (col0 + cl + 8 i) and its
+    // rows' steps (one per lane and chunk) are fetched a tile ahead.
+    Tile next{};
+    float ws_n[4], bs_n[4], as_n[C::MY_CHUNKS];
+    auto fetch = [&](int tile) {
+      if (tile >= num_tiles) return;
+      locate(p, off, tiles, tile, next);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int n = col0 + cl + 8 * i;
-        const int64_t sn = (int64_t)t.e * p.N + n;
+        const int n = next.n0 + rank * CH + quarter * 32 + cl + 8 * i;
+        const int64_t sn = (int64_t)next.e * p.N + n;
         const bool ok = n < p.N && in_bounds(sn, 1, (int64_t)p.E * p.N, p.status);
-        ws[i] = ok ? __ldcg(p.w_scale + sn) : 0.0f;
-        bs[i] = ok && p.bias ? __ldcg(p.bias + sn) : 0.0f;
+        ws_n[i] = ok ? __ldcg(p.w_scale + sn) : 0.0f;
+        bs_n[i] = ok && p.bias ? __ldcg(p.bias + sn) : 0.0f;
       }
-      // the steps of this warp's rows, one per lane and chunk, in shared memory
-      // before the accumulator is full
-      __syncwarp();  // the last tile's are read
 #pragma unroll
       for (int i = 0; i < C::MY_CHUNKS; ++i) {
         const int c = (chunk0 + i * (EPI_W / 4)) * 32 + lane;
-        as_w[i * 32 + lane] = __ldcg(p.act_scale + (p.per_token ? t.row0 + min(c, t.rows - 1) : 0));
+        as_n[i] = __ldcg(p.act_scale + (p.per_token ? next.row0 + min(c, next.rows - 1) : 0));
       }
+    };
+    fetch(unit0);
+    for (int tile = unit0; tile < num_tiles; tile += units) {
+      const Tile t = next;
+      const int col0 = t.n0 + rank * CH + quarter * 32;
+      float ws[4], bs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ws[i] = ws_n[i];
+        bs[i] = bs_n[i];
+      }
+      __syncwarp();  // the last tile's steps are read
+#pragma unroll
+      for (int i = 0; i < C::MY_CHUNKS; ++i) as_w[i * 32 + lane] = as_n[i];
       __syncwarp();
+      fetch(tile + units);
       if (!tc::mbar_wait(tfull_bar(abuf), aphase, abort_flag, kWaitNs, p.status)) break;
       tc::tc_fence_after();
       const float* as_c = as_w;
