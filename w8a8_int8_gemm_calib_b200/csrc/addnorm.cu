@@ -62,14 +62,15 @@ __device__ __forceinline__ void store_chunk(uint16_t* p, const Raw8<uint16_t>& h
 
 // CM > 0: a thread's chunks of h (at most CM) stay in registers in their
 // storage form, its gamma in shared memory, and the next row's x and r are
-// loaded while this row is reduced and quantized.  CM == 0: h is read back
-// from global memory, each chunk by the thread that wrote it.
+// loaded while this row is reduced and quantized.  CM == 0, wider rows: h is
+// read back from L2, each chunk by the thread that wrote it (h in shared
+// memory instead measured no faster: fewer rows share an SM).
 //
 // A CTA is one 128-thread slice, so rows in different phases share an SM.
 template <typename T, int CM, int MODE>
 __global__ void __launch_bounds__(kSlice) addnorm_kernel(const AddNormArgs a) {
-  __shared__ float red[2][4];
-  extern __shared__ __align__(16) float gs[];  // CM > 0: [2 CM][128] float4
+  __shared__ float red[2][2][4];  // [row parity][reduction][warp]
+  extern __shared__ __align__(16) float gs[];  // CM > 0: gamma, [2 CM][128] float4
   pdl_launch_dependents();
   pdl_wait();
   const int j = threadIdx.x, w = j >> 5, lane = j & 31;
@@ -108,7 +109,8 @@ __global__ void __launch_bounds__(kSlice) addnorm_kernel(const AddNormArgs a) {
   }
   const float static_inv = MODE == ROW_STATIC ? __fdiv_rn(1.0f, __ldcg(a.scale)) : 0.0f;
 
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, parity ^= 1) {
     const int64_t base = row * K;
     float p = 0.0f;
     // h = x + r, stored, and its sum of squares
@@ -128,20 +130,30 @@ __global__ void __launch_bounds__(kSlice) addnorm_kernel(const AddNormArgs a) {
       }
       load_rows(row + gridDim.x);
     } else {
-      for (int64_t c = j; c < nchunk; c += kSlice) {
-        Raw8<T> xc{}, rc{}, hc;
-        if (in_bounds(base + c * 8, 8, size, a.status)) {
-          load_raw(x + base + c * 8, xc);
-          load_raw(res + base + c * 8, rc);
+      constexpr int U = sizeof(T) == 2 ? 4 : 2;  // 128 bytes a thread in flight
+      for (int64_t c0 = j; c0 < nchunk; c0 += U * kSlice) {
+        Raw8<T> xc[U], rc[U], hc;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t c = c0 + u * kSlice;
+          if (c < nchunk && in_bounds(base + c * 8, 8, size, a.status)) {
+            load_raw(x + base + c * 8, xc[u]);
+            load_raw(res + base + c * 8, rc[u]);
+          }
         }
-        first(c, xc, rc, hc);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t c = c0 + u * kSlice;
+          if (c < nchunk) first(c, xc[u], rc[u], hc);
+        }
       }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) p = __fadd_rn(p, __shfl_xor_sync(0xffffffffu, p, o));
-    if (lane == 0) red[0][w] = p;
+    float (&rd)[2][4] = red[parity];  // read before the next row's barriers
+    if (lane == 0) rd[0][w] = p;
     __syncthreads();
-    const float ss = __fadd_rn(__fadd_rn(red[0][0], red[0][2]), __fadd_rn(red[0][1], red[0][3]));
+    const float ss = __fadd_rn(__fadd_rn(rd[0][0], rd[0][2]), __fadd_rn(rd[0][1], rd[0][3]));
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, kf), a.eps)));
 
     // f(c, y[8]) over the thread's chunks
@@ -167,6 +179,7 @@ __global__ void __launch_bounds__(kSlice) addnorm_kernel(const AddNormArgs a) {
           }
         }
       } else {
+#pragma unroll 4
         for (int64_t c = j; c < nchunk; c += kSlice) {
           Raw8<T> hc{};
           if (in_bounds(base + c * 8, 8, size, a.status)) load_raw_cached(hp + base + c * 8, hc);
@@ -190,9 +203,9 @@ __global__ void __launch_bounds__(kSlice) addnorm_kernel(const AddNormArgs a) {
         });
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) red[1][w] = m;
+        if (lane == 0) rd[1][w] = m;
         __syncthreads();
-        m = fmaxf(fmaxf(red[1][0], red[1][2]), fmaxf(red[1][1], red[1][3]));
+        m = fmaxf(fmaxf(rd[1][0], rd[1][2]), fmaxf(rd[1][1], rd[1][3]));
         const float delta = __fdiv_rn(fmaxf(m, 1e-7f), 127.0f);
         inv = __fdiv_rn(1.0f, delta);
         if (j == 0 && in_bounds(row, 1, a.T, a.status)) a.scale[row] = delta;
@@ -205,9 +218,6 @@ __global__ void __launch_bounds__(kSlice) addnorm_kernel(const AddNormArgs a) {
         if (in_bounds(base + c * 8, 8, size, a.status)) store_codes(a.q + base + c * 8, b);
       });
     }
-    // the next row's sum of squares overwrites red[0], which every warp read
-    // before the barrier of the peak (or reads before this one)
-    if constexpr (MODE != ROW_DYNAMIC) __syncthreads();
   }
   if constexpr (MODE == ROW_PEAK) {
 #pragma unroll
