@@ -299,9 +299,9 @@ constexpr int kBatch = 8;  // assignments of a token whose rows are in flight to
 // 16384 tokens x 8 rows of 4096 bf16 combined in 246 / 221 / 246 us with
 // 3 / 4 / 5 (at 5 the loads no longer fit the registers).
 constexpr int kCombineBlocks = 4;
-// 8192 x 8 rows of 4096 bf16, with the rows' gradients: 379 / 334 / 334 us
-// with 2 / 3 / 4.
-constexpr int kGradBlocks = 3;
+// The gradients of 8192 x 8 rows of 4096 bf16 take 217 / 211 / 300 us, of
+// 512 x 2 rows 8.5 / 6.4 / 11.5 us, with 3 / 4 / 5 (at 5 the loads spill).
+constexpr int kGradBlocks = 4;
 
 // the sorted row of assignment (t, c), or -1
 __device__ __forceinline__ int64_t place(const MoeArgs& a, int64_t t, int c) {
