@@ -25,12 +25,13 @@ LIB_DEBUG = os.path.join(HERE, "libsq_b200_debug.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cpp", "status.cu", "rowops.cu", "rowpipe.cu", "rowreg.cu", "addnorm.cu", "moe.cu",
-           "gemm.cu", "grouped.cu", "probe.cu"]
+           "combine.cu", "gemm.cu", "grouped.cu", "probe.cu"]
 # The row pipeline's packed fp32 multiplies and adds must stay separately
 # rounded (the INT8 codes are bit-exact against the oracle); its one intended
 # fused multiply-add is an explicit intrinsic, which this flag leaves alone.
 EXTRA_FLAGS = {"rowpipe.cu": ["-fmad=false"]}
-HEADERS = ["sq_internal.h", "sq_device.cuh", "tc_ptx.cuh", "launch.cuh", "tmaps.h"]
+HEADERS = ["sq_internal.h", "sq_device.cuh", "tc_ptx.cuh", "launch.cuh", "tmaps.h",
+           "moe.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", "-I", INCLUDE, "-I", CSRC]

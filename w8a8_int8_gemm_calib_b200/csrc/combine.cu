@@ -1,0 +1,329 @@
+// combine.cu -- the experts' rows back to their tokens, and the gradient.
+//
+//   combine  y[t] = rnd(res[t] + sum_c w[t,c] z[pos[t,c]])
+//   grad     dz[pos[t,c]] = rnd(w[t,c] dy[t]),
+//            dw[t,c] = sum_n dy[t,n] z[pos[t,c],n]
+//
+// Both walk the tokens: a token's row is touched once, its top_k rows are
+// read (and written), and every sum runs in one fixed order.
+//
+// Bound: HBM -- top_k + 2 rows a token, 2 top_k + 1 for the gradient.  Rows lie
+// anywhere, so what counts is bytes in flight: a thread has eight 16-byte
+// loads outstanding, of one token's rows or, with few rows a token, of
+// several tokens', and the places of the next step are loaded before the
+// rows of this one.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "launch.cuh"
+#include "moe.cuh"
+#include "sq_device.cuh"
+#include "sq_internal.h"
+
+namespace sq {
+
+namespace {
+
+constexpr int kBatch = 8;  // assignments whose rows are in flight together
+
+// A thread's part of a row: U pieces of G bytes (V elements each), the block's
+// threads side by side in each.  G is 16, or what the rows' pitch keeps
+// aligned (4, or a bf16's 2): then four pieces.
+template <typename T, int G>
+struct Part {
+  static constexpr int V = G / (int)sizeof(T);
+  static constexpr int U = G == 16 ? 1 : 4;
+  static constexpr int E = U * V;
+  uint32_t w[G == 16 ? 4 : U];
+
+  __device__ __forceinline__ void load(const T* row, const int (&c)[U], int n) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c[u] >= n) continue;
+      if constexpr (G == 16) {
+        const uint4 q = ld_stream_u4(row + c[u]);
+        w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+      } else if constexpr (G == 4) {
+        w[u] = __ldcg(reinterpret_cast<const unsigned int*>(row + c[u]));
+      } else {
+        w[u] = __ldcg(reinterpret_cast<const unsigned short*>(row + c[u]));
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[E]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (G == 2) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = bf16lo(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        v[2 * i] = bf16lo(w[i]);
+        v[2 * i + 1] = bf16hi(w[i]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(T* row, const int (&c)[U], int n, const float (&v)[E]) {
+    uint32_t o[G == 16 ? 4 : U];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = __float_as_uint(v[i]);
+    } else if constexpr (G == 2) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+        o[i] = *reinterpret_cast<const uint16_t*>(&h);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c[u] >= n) continue;
+      if constexpr (G == 16)
+        *reinterpret_cast<uint4*>(row + c[u]) = make_uint4(o[0], o[1], o[2], o[3]);
+      else if constexpr (G == 4)
+        *reinterpret_cast<uint32_t*>(row + c[u]) = o[u];
+      else
+        *reinterpret_cast<uint16_t*>(row + c[u]) = (uint16_t)o[u];
+    }
+  }
+};
+
+// In a bounds-checked build: the row lies in a tensor of `rows` rows.
+__device__ __forceinline__ bool row_ok(const MoeArgs& a, int64_t row, int64_t rows) {
+  return in_bounds(row * a.N, a.N, rows * a.N, a.status);
+}
+
+// P tokens a step, their first kBatch / P assignments each: P = 4 for top_k
+// up to 2, 2 up to 4, else 1, with as many steps of 8 as top_k takes.  Lane b
+// of every warp holds the place and weight of the step's assignment b.
+template <int P>
+struct Step {
+  static constexpr int KK = kBatch / P;
+  int row;
+  float wt;
+  __device__ __forceinline__ void fetch(const MoeArgs& a, int64_t t0, int k0, int lane) {
+    const int b = lane & (kBatch - 1);
+    const int64_t t = t0 + b / KK;
+    const int k = t < a.T ? k0 + b % KK : a.top_k;
+    wt = a.w && k < a.top_k ? __ldcg(a.w + t * a.top_k + k) : 1.0f;
+    row = (int)place(a, t, k);
+  }
+};
+
+// Resident blocks per SM (registers: 64 a thread, 80 with several tokens a
+// step).  16384 x 8 rows of 4096 bf16 are combined in 246 / 221 / 246 us with
+// 3 / 4 / 5 blocks, the gradients of 8192 x 8 rows take 217 / 211 / 300 us.
+template <int P>
+constexpr int kBlocks = P == 1 ? 4 : 3;
+
+template <typename T, int G, int P>
+__global__ void __launch_bounds__(kRowThreads, kBlocks<P>) combine_kernel(const MoeArgs a) {
+  using L = Part<T, G>;
+  constexpr int KK = Step<P>::KK;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, n = (int)a.N;
+  int c[L::U];
+#pragma unroll
+  for (int u = 0; u < L::U; ++u)
+    c[u] = ((int)(blockIdx.y * L::U + u) * (int)blockDim.x + (int)threadIdx.x) * L::V;
+  const T* z = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.res);
+  T* y = static_cast<T*>(a.out);
+  Step<P> next;
+  next.fetch(a, (int64_t)blockIdx.x * P, 0, lane);
+  for (int64_t t0 = (int64_t)blockIdx.x * P; t0 < a.T; t0 += (int64_t)gridDim.x * P) {
+    L rs[P];
+    float acc[L::E];
+    for (int k0 = 0; k0 < a.top_k; k0 += KK) {
+      const Step<P> now = next;
+      if (k0 + KK < a.top_k) next.fetch(a, t0, k0 + KK, lane);
+      else next.fetch(a, t0 + (int64_t)gridDim.x * P, 0, lane);
+      L raw[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int r = __shfl_sync(0xffffffffu, now.row, b);
+        if (r >= 0 && row_ok(a, r, a.R)) raw[b].load(z + r * a.N, c, n);
+      }
+      if (k0 == 0) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          if (res && t0 + p < a.T && row_ok(a, t0 + p, a.T)) rs[p].load(res + (t0 + p) * a.N, c, n);
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (k0 == 0) {
+          if (res) {
+            rs[p].get(acc);
+          } else {
+#pragma unroll
+            for (int e = 0; e < L::E; ++e) acc[e] = 0.0f;
+          }
+        }
+#pragma unroll
+        for (int b = p * KK; b < (p + 1) * KK; ++b) {
+          const int r = __shfl_sync(0xffffffffu, now.row, b);
+          const float wt = __shfl_sync(0xffffffffu, now.wt, b);
+          if (r < 0) continue;
+          float v[L::E];
+          raw[b].get(v);
+          if (a.w) {
+#pragma unroll
+            for (int e = 0; e < L::E; ++e) acc[e] = __fmaf_rn(wt, v[e], acc[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < L::E; ++e) acc[e] = __fadd_rn(acc[e], v[e]);
+          }
+        }
+        if (k0 + KK >= a.top_k && t0 + p < a.T && row_ok(a, t0 + p, a.T))
+          L::put(y + (t0 + p) * a.N, c, n, acc);
+      }
+    }
+  }
+}
+
+// Eight sums over 32 lanes: in the first three steps a lane passes on the half
+// of its sums that the other lane keeps, so 9 shuffles do instead of 40; the
+// sum of b ends in lanes 4 b .. 4 b + 3.
+__device__ __forceinline__ float lanes_sum8(float (&v)[kBatch], int lane) {
+#pragma unroll
+  for (int s = 4; s >= 1; s >>= 1) {
+    const int o = s * 4;  // 16, 8, 4
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
+      v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  const float r = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+  return __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
+}
+
+// A block has whole rows.  Each thread adds its columns' products in
+// increasing column, then lanes and warps are combined: one fixed order, fp32.
+template <typename T, int G, int P>
+__global__ void __launch_bounds__(kRowThreads, kBlocks<P>) combine_grad_kernel(const MoeArgs a) {
+  using L = Part<T, G>;
+  constexpr int KK = Step<P>::KK;
+  __shared__ float part[2][kRowThreads / 32][kBatch];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nt = blockDim.x, n = (int)a.N;
+  const T* dy = static_cast<const T*>(a.res);
+  const T* z = static_cast<const T*>(a.x);
+  T* dz = static_cast<T*>(a.out);
+  const bool want_w = a.dw != nullptr;
+  int parity = 0;
+  Step<P> next;
+  next.fetch(a, (int64_t)blockIdx.x * P, 0, lane);
+  for (int64_t t0 = (int64_t)blockIdx.x * P; t0 < a.T; t0 += (int64_t)gridDim.x * P) {
+    for (int k0 = 0; k0 < a.top_k; k0 += KK) {
+      const Step<P> now = next;
+      if (k0 + KK < a.top_k) next.fetch(a, t0, k0 + KK, lane);
+      else next.fetch(a, t0 + (int64_t)gridDim.x * P, 0, lane);
+      float dot[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) dot[b] = 0.0f;
+      // whole warps run every step (the places are passed by shuffle)
+      for (int c0 = 0; c0 < n; c0 += nt * L::E) {  // n <= 2^20
+        int c[L::U];
+#pragma unroll
+        for (int u = 0; u < L::U; ++u) c[u] = c0 + (u * nt + (int)threadIdx.x) * L::V;
+        L dr[P], zr[kBatch];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          if (t0 + p < a.T && row_ok(a, t0 + p, a.T)) dr[p].load(dy + (t0 + p) * a.N, c, n);
+        if (want_w) {
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int r = __shfl_sync(0xffffffffu, now.row, b);
+            if (r >= 0 && row_ok(a, r, a.R)) zr[b].load(z + r * a.N, c, n);
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float d[L::E];
+          dr[p].get(d);
+#pragma unroll
+          for (int b = p * KK; b < (p + 1) * KK; ++b) {
+            const int r = __shfl_sync(0xffffffffu, now.row, b);
+            const float wt = __shfl_sync(0xffffffffu, now.wt, b);
+            if (r < 0) continue;
+            float v[L::E];
+            if (want_w) {
+              zr[b].get(v);
+#pragma unroll
+              for (int e = 0; e < L::E; ++e)
+                if (c[e / L::V] < n) dot[b] = __fmaf_rn(d[e], v[e], dot[b]);
+            }
+            if (dz && row_ok(a, r, a.R)) {
+#pragma unroll
+              for (int e = 0; e < L::E; ++e) v[e] = __fmul_rn(wt, d[e]);
+              L::put(dz + r * a.N, c, n, v);
+            }
+          }
+        }
+      }
+      if (!want_w) continue;
+      const float s8 = lanes_sum8(dot, lane);
+      if ((lane & 3) == 0) part[parity][warp][lane >> 2] = s8;
+      __syncthreads();
+      if (threadIdx.x < kBatch) {
+        const int b = threadIdx.x, k = k0 + b % KK;
+        const int64_t t = t0 + b / KK;
+        if (t < a.T && k < a.top_k && in_bounds(t * a.top_k + k, 1, a.T * a.top_k, a.status)) {
+          float s = 0.0f;
+          for (int w = 0; w < (nt >> 5); ++w) s = __fadd_rn(s, part[parity][w][b]);
+          a.dw[t * a.top_k + k] = s;
+        }
+      }
+      parity ^= 1;  // the next step's sums do not wait for these reads
+    }
+  }
+}
+
+// Blocks: as many as are resident, if there are tokens for them.
+template <typename T, int G, int P>
+cudaError_t launch_gp(const MoeArgs& a, bool grad, cudaStream_t st) {
+  using L = Part<T, G>;
+  const int64_t pieces = (a.N + L::E - 1) / L::E;  // threads that cover a row
+  const unsigned nt = row_threads(pieces);
+  const int64_t segs = grad ? 1 : (pieces + nt - 1) / nt;
+  const int64_t steps = (a.T + P - 1) / P;
+  int64_t walk = (kBlocks<P> * (int64_t)sm_count() * (kRowThreads / nt) + segs - 1) / segs;
+  if (walk > steps) walk = steps;
+  const dim3 grid((unsigned)walk, (unsigned)segs);
+  return grad ? launch_pdl(combine_grad_kernel<T, G, P>, grid, dim3(nt), 0, st, a)
+              : launch_pdl(combine_kernel<T, G, P>, grid, dim3(nt), 0, st, a);
+}
+
+template <typename T, int G>
+cudaError_t launch_g(const MoeArgs& a, bool grad, cudaStream_t st) {
+  if (a.top_k <= 2) return launch_gp<T, G, 4>(a, grad, st);
+  if (a.top_k <= 4) return launch_gp<T, G, 2>(a, grad, st);
+  return launch_gp<T, G, 1>(a, grad, st);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_combine(MoeArgs a, sq_dtype t, bool grad, cudaStream_t st) {
+  a.status = status_word();
+  if (!a.status) return cudaErrorInvalidDevice;
+  if (t == SQ_BF16)
+    return a.N % 8 == 0   ? launch_g<uint16_t, 16>(a, grad, st)
+           : a.N % 2 == 0 ? launch_g<uint16_t, 4>(a, grad, st)
+                          : launch_g<uint16_t, 2>(a, grad, st);
+  return a.N % 4 == 0 ? launch_g<float, 16>(a, grad, st) : launch_g<float, 4>(a, grad, st);
+}
+
+}  // namespace sq

@@ -1,24 +1,22 @@
-// moe.cu -- tokens sorted by expert and back: the routing around a W8A8
-// linear whose weights are experts chosen per token.
+// moe.cu -- tokens sorted by expert, and their codes copied to the sorted
+// rows: the way to a W8A8 linear whose weights are experts chosen per token.
 //
 //   sort     offsets[e] = #{i : id_i < e},  pos_i = offsets[id_i] +
 //            #{j < i : id_j = id_i}   over the live assignments i = (t, c)
 //   gather   xs[pos_i] = x[t]  (and its step)
-//   combine  y[t] = rnd(res[t] + sum_c w[t,c] z[pos_i])
-//   grad     dz[pos_i] = rnd(w[t,c] dy[t]),  dw[t,c] = sum_n dy[t,n] z[pos_i,n]
 //
-// Everything is indexed by token: a token's row is read once and its top_k
-// rows are written (gather, grad) or read (combine, grad), so no step needs
-// the inverse order, and every sum runs in one fixed order.
+// Places are indexed by token: a token's row is read once and its top_k
+// copies are written, and neither this nor the way back (combine.cu) needs
+// the inverse order.
 //
-// Bound: HBM for the row steps -- the sort moves 12 bytes per assignment and
-// is bound by its launches.
-#include <cuda_bf16.h>
+// Bound: the gather by HBM; the sort moves 12 bytes per assignment and is
+// bound by its launches.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "launch.cuh"
 #include "sq_device.cuh"
+#include "moe.cuh"
 #include "sq_internal.h"
 
 namespace sq {
@@ -242,74 +240,6 @@ cudaError_t launch_sort_t(SortArgs a, cudaStream_t st) {
 }
 
 // ====================================================================== rows
-// 16 bytes of a row, or one element where rows do not keep 16-byte alignment
-template <typename T, bool VEC> struct Lane;
-template <> struct Lane<uint16_t, true> {
-  static constexpr int V = 8;
-  uint4 a;
-  __device__ __forceinline__ void load(const uint16_t* p) { a = ld_stream_u4(p); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    Raw8<uint16_t> r;
-    r.a = a;
-    unpack(r, v);
-  }
-  static __device__ __forceinline__ void put(uint16_t* p, const float (&v)[8]) {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      h[i] = *reinterpret_cast<uint32_t*>(&t);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
-  }
-};
-template <> struct Lane<float, true> {
-  static constexpr int V = 4;
-  uint4 a;
-  __device__ __forceinline__ void load(const float* p) { a = ld_stream_u4(p); }
-  __device__ __forceinline__ void get(float (&v)[4]) const {
-    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
-    v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-  }
-  static __device__ __forceinline__ void put(float* p, const float (&v)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  }
-};
-template <> struct Lane<uint16_t, false> {
-  static constexpr int V = 1;
-  uint16_t a;
-  __device__ __forceinline__ void load(const uint16_t* p) { a = __ldcg(p); }
-  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __uint_as_float((uint32_t)a << 16); }
-  static __device__ __forceinline__ void put(uint16_t* p, const float (&v)[1]) {
-    __nv_bfloat16 t = __float2bfloat16_rn(v[0]);
-    *p = *reinterpret_cast<uint16_t*>(&t);
-  }
-};
-template <> struct Lane<float, false> {
-  static constexpr int V = 1;
-  float a;
-  __device__ __forceinline__ void load(const float* p) { a = __ldcg(p); }
-  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
-  static __device__ __forceinline__ void put(float* p, const float (&v)[1]) { *p = v[0]; }
-};
-
-constexpr int kRowThreads = 256;
-constexpr int kBatch = 8;  // assignments of a token whose rows are in flight together
-// Resident blocks per SM, each thread with kBatch 16-byte loads in flight.
-// 16384 tokens x 8 rows of 4096 bf16 combined in 246 / 221 / 246 us with
-// 3 / 4 / 5 (at 5 the loads no longer fit the registers).
-constexpr int kCombineBlocks = 4;
-// The gradients of 8192 x 8 rows of 4096 bf16 take 217 / 211 / 300 us, of
-// 512 x 2 rows 8.5 / 6.4 / 11.5 us, with 3 / 4 / 5 (at 5 the loads spill).
-constexpr int kGradBlocks = 4;
-
-// the sorted row of assignment (t, c), or -1
-__device__ __forceinline__ int64_t place(const MoeArgs& a, int64_t t, int c) {
-  if (c >= a.top_k || !in_bounds(t * a.top_k + c, 1, a.T * a.top_k, a.status)) return -1;
-  const int64_t r = __ldcg(a.pos + t * a.top_k + c);
-  return r >= 0 && r < a.R ? r : -1;
-}
-
 // ---------------------------------------------------------------- gather
 // U: the unit a row is copied in (16 bytes, or its element)
 template <typename U>
@@ -331,201 +261,6 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const MoeArgs a) {
     const int64_t r = place(a, t, k);
     if (r >= 0 && in_bounds(r * n + c, 1, a.R * n, a.status)) static_cast<U*>(a.out)[r * n + c] = v;
   }
-}
-
-// ---------------------------------------------------------------- combine
-// A block keeps its columns and walks the tokens; every lane of a warp holds
-// the place and weight of one assignment (32 at a time), and the next
-// token's are loaded before this token's rows, so that a row load waits for
-// no place.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, kCombineBlocks) combine_kernel(const MoeArgs a) {
-  using L = Lane<T, VEC>;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * L::V;
-  const bool col = c < a.N;
-  const T* z = static_cast<const T*>(a.x) + c;
-  int row = -1;
-  float wt = 1.0f;
-  auto fetch = [&](int64_t t, int k0) {
-    const int k = t < a.T ? k0 + lane : a.top_k;
-    if (a.w && k < a.top_k) wt = __ldcg(a.w + t * a.top_k + k);
-    row = (int)place(a, t, k);
-  };
-  fetch(blockIdx.x, 0);
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const bool in = col && in_bounds(t * a.N + c, L::V, a.T * a.N, a.status);
-    L res;
-    if (a.res && in) res.load(static_cast<const T*>(a.res) + t * a.N + c);
-    float acc[L::V];
-#pragma unroll
-    for (int e = 0; e < L::V; ++e) acc[e] = 0.0f;
-    for (int k0 = 0; k0 < a.top_k; k0 += 32) {
-      const int rows = row;
-      const float wts = wt;
-      // the next 32, or the next token's
-      if (k0 + 32 < a.top_k) fetch(t, k0 + 32);
-      else fetch(t + gridDim.x, 0);
-      const int n = min(32, a.top_k - k0);
-      for (int b0 = 0; b0 < n; b0 += kBatch) {
-        L raw[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int r = __shfl_sync(0xffffffffu, rows, b0 + b);
-          if (r >= 0 && col && in_bounds(r * a.N + c, L::V, a.R * a.N, a.status))
-            raw[b].load(z + r * a.N);
-        }
-        if (k0 == 0 && b0 == 0 && a.res && in) res.get(acc);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int r = __shfl_sync(0xffffffffu, rows, b0 + b);
-          const float wb = __shfl_sync(0xffffffffu, wts, b0 + b);
-          if (r < 0) continue;
-          float v[L::V];
-          raw[b].get(v);
-          if (a.w) {
-#pragma unroll
-            for (int e = 0; e < L::V; ++e) acc[e] = __fmaf_rn(wb, v[e], acc[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < L::V; ++e) acc[e] = __fadd_rn(acc[e], v[e]);
-          }
-        }
-      }
-    }
-    if (in) L::put(static_cast<T*>(a.out) + t * a.N + c, acc);
-  }
-}
-
-// ---------------------------------------------------------------- grad
-// A block walks the tokens, its threads the columns.  Each thread adds its
-// columns' products in increasing column, lanes and then warps are combined
-// in one fixed order, fp32.
-//
-// Eight sums over 32 lanes: in the first three steps a lane passes on the half
-// of its sums that the other lane keeps, so 9 shuffles do instead of 40; the
-// sum of b ends in lanes 4 b' .. 4 b' + 3, b' = b with its three bits in
-// lane bits 4, 3, 2.
-__device__ __forceinline__ float lanes_sum8(float (&v)[kBatch], int lane) {
-#pragma unroll
-  for (int s = 4; s >= 1; s >>= 1) {
-    const int o = s * 4;  // 16, 8, 4
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < s; ++i) {
-      const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
-      v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, o));
-    }
-  }
-  float r = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
-  return __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
-}
-
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, kGradBlocks) combine_grad_kernel(const MoeArgs a) {
-  using L = Lane<T, VEC>;
-  __shared__ float part[2][kRowThreads / 32][kBatch];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nt = blockDim.x;
-  const T* dy = static_cast<const T*>(a.res);
-  const T* z = static_cast<const T*>(a.x);
-  T* dz = static_cast<T*>(a.out);
-  const bool want_w = a.dw != nullptr;
-  const int n = (int)a.N;
-  int parity = 0;
-  int row = -1;
-  float wt = 1.0f;
-  // place and weight of assignment k0 + (lane mod 8), one batch ahead
-  auto fetch = [&](int64_t t, int k0) {
-    const int k = t < a.T ? k0 + (lane & (kBatch - 1)) : a.top_k;
-    if (a.w && k < a.top_k) wt = __ldcg(a.w + t * a.top_k + k);
-    row = (int)place(a, t, k);
-  };
-  fetch(blockIdx.x, 0);
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    for (int k0 = 0; k0 < a.top_k; k0 += kBatch) {
-      const int rows = row;
-      const float wts = wt;
-      if (k0 + kBatch < a.top_k) fetch(t, k0 + kBatch);
-      else fetch(t + gridDim.x, 0);
-      float dot[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) dot[b] = 0.0f;
-      // whole warps run every step (the places are passed by shuffle)
-      for (int c0 = warp * 32 * L::V; c0 < n; c0 += nt * L::V) {  // n <= 2^20
-        const int c = c0 + lane * L::V;
-        const bool in = c < n && in_bounds(t * a.N + c, L::V, a.T * a.N, a.status);
-        L dr, zr[kBatch];
-        if (in) dr.load(dy + t * a.N + c);
-        if (want_w) {
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int r = __shfl_sync(0xffffffffu, rows, b);
-            if (r >= 0 && in && in_bounds(r * a.N + c, L::V, a.R * a.N, a.status))
-              zr[b].load(z + r * a.N + c);
-          }
-        }
-        float d[L::V];
-        dr.get(d);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int r = __shfl_sync(0xffffffffu, rows, b);
-          const float wb = __shfl_sync(0xffffffffu, wts, b);
-          if (r < 0 || !in) continue;
-          float v[L::V];
-          if (want_w) {
-            zr[b].get(v);
-#pragma unroll
-            for (int e = 0; e < L::V; ++e) dot[b] = __fmaf_rn(d[e], v[e], dot[b]);
-          }
-          if (dz && in_bounds(r * a.N + c, L::V, a.R * a.N, a.status)) {
-#pragma unroll
-            for (int e = 0; e < L::V; ++e) v[e] = __fmul_rn(wb, d[e]);
-            L::put(dz + r * a.N + c, v);
-          }
-        }
-      }
-      if (!want_w) continue;
-      const float s8 = lanes_sum8(dot, lane);
-      if ((lane & 3) == 0) part[parity][warp][lane >> 2] = s8;
-      __syncthreads();
-      if (threadIdx.x < kBatch && k0 + (int)threadIdx.x < a.top_k &&
-          in_bounds(t * a.top_k + k0 + threadIdx.x, 1, a.T * a.top_k, a.status)) {
-        float s = 0.0f;
-        for (int w = 0; w < (nt >> 5); ++w) s = __fadd_rn(s, part[parity][w][threadIdx.x]);
-        a.dw[t * a.top_k + k0 + threadIdx.x] = s;
-      }
-      parity ^= 1;  // the next batch's sums do not wait for these reads
-    }
-  }
-}
-
-unsigned row_threads(int64_t n) {
-  return n >= kRowThreads ? (unsigned)kRowThreads : (unsigned)((n + 31) / 32 * 32);
-}
-
-template <typename T>
-cudaError_t launch_combine_t(const MoeArgs& a, bool grad, cudaStream_t st) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const bool vec = a.N % V == 0;
-  const int64_t n = vec ? a.N / V : a.N;
-  const unsigned nt = row_threads(n);
-  if (grad) {
-    int64_t walk = kGradBlocks * (int64_t)sm_count() * (kRowThreads / nt);
-    if (walk > a.T) walk = a.T;
-    const dim3 grid((unsigned)walk);
-    return vec ? launch_pdl(combine_grad_kernel<T, true>, grid, dim3(nt), 0, st, a)
-               : launch_pdl(combine_grad_kernel<T, false>, grid, dim3(nt), 0, st, a);
-  }
-  const int64_t segs = (n + nt - 1) / nt;
-  int64_t walk = (kCombineBlocks * (int64_t)sm_count() * (kRowThreads / nt) + segs - 1) / segs;
-  if (walk > a.T) walk = a.T;
-  const dim3 grid((unsigned)walk, (unsigned)segs);
-  return vec ? launch_pdl(combine_kernel<T, true>, grid, dim3(nt), 0, st, a)
-             : launch_pdl(combine_kernel<T, false>, grid, dim3(nt), 0, st, a);
 }
 
 }  // namespace
@@ -558,13 +293,6 @@ cudaError_t launch_moe_gather(MoeArgs a, size_t elem, cudaStream_t st) {
   if (elem == 1) return launch_pdl(gather_kernel<uint8_t>, grid, dim3(nt), 0, st, a);
   if (elem == 2) return launch_pdl(gather_kernel<uint16_t>, grid, dim3(nt), 0, st, a);
   return launch_pdl(gather_kernel<uint32_t>, grid, dim3(nt), 0, st, a);
-}
-
-cudaError_t launch_moe_combine(MoeArgs a, sq_dtype t, bool grad, cudaStream_t st) {
-  a.status = status_word();
-  if (!a.status) return cudaErrorInvalidDevice;
-  return t == SQ_BF16 ? launch_combine_t<uint16_t>(a, grad, st)
-                      : launch_combine_t<float>(a, grad, st);
 }
 
 }  // namespace sq
