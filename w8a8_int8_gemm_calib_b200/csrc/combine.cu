@@ -102,8 +102,8 @@ __device__ __forceinline__ bool row_ok(const MoeArgs& a, int64_t row, int64_t ro
   return in_bounds(row * a.N, a.N, rows * a.N, a.status);
 }
 
-// P tokens a step, their first kBatch / P assignments each: P = 4 for top_k
-// up to 2, 2 up to 4, else 1, with as many steps of 8 as top_k takes.  Lane b
+// P tokens a step, their first kBatch / P assignments each: P may be 4 for
+// top_k up to 2, 2 up to 4, else it is 1, with as many steps of 8 as top_k takes.  Lane b
 // of every warp holds the place and weight of the step's assignment b.
 template <int P>
 struct Step {
@@ -292,25 +292,46 @@ __global__ void __launch_bounds__(kRowThreads, kBlocks<P>) combine_grad_kernel(c
   }
 }
 
-// Blocks: as many as are resident, if there are tokens for them.
+// Threads per block, blocks across a row, blocks that are resident at once
+// and steps over the tokens, for P tokens a step.
+struct Plan {
+  unsigned nt;
+  int64_t segs, resident, steps;
+};
 template <typename T, int G, int P>
-cudaError_t launch_gp(const MoeArgs& a, bool grad, cudaStream_t st) {
-  using L = Part<T, G>;
-  const int64_t pieces = (a.N + L::E - 1) / L::E;  // threads that cover a row
-  const unsigned nt = row_threads(pieces);
-  const int64_t segs = grad ? 1 : (pieces + nt - 1) / nt;
-  const int64_t steps = (a.T + P - 1) / P;
-  int64_t walk = (kBlocks<P> * (int64_t)sm_count() * (kRowThreads / nt) + segs - 1) / segs;
-  if (walk > steps) walk = steps;
-  const dim3 grid((unsigned)walk, (unsigned)segs);
-  return grad ? launch_pdl(combine_grad_kernel<T, G, P>, grid, dim3(nt), 0, st, a)
-              : launch_pdl(combine_kernel<T, G, P>, grid, dim3(nt), 0, st, a);
+Plan plan(const MoeArgs& a, bool grad) {
+  Plan q;
+  const int64_t pieces = (a.N + Part<T, G>::E - 1) / Part<T, G>::E;  // threads that cover a row
+  q.nt = row_threads(pieces);
+  q.segs = grad ? 1 : (pieces + q.nt - 1) / q.nt;
+  q.resident = kBlocks<P> * (int64_t)sm_count() * (kRowThreads / q.nt);
+  q.steps = (a.T + P - 1) / P;
+  return q;
 }
 
+template <typename T, int G, int P>
+cudaError_t launch_gp(const MoeArgs& a, bool grad, cudaStream_t st) {
+  const Plan q = plan<T, G, P>(a, grad);
+  int64_t walk = (q.resident + q.segs - 1) / q.segs;
+  if (walk > q.steps) walk = q.steps;
+  const dim3 grid((unsigned)walk, (unsigned)q.segs);
+  return grad ? launch_pdl(combine_grad_kernel<T, G, P>, grid, dim3(q.nt), 0, st, a)
+              : launch_pdl(combine_kernel<T, G, P>, grid, dim3(q.nt), 0, st, a);
+}
+
+// Several tokens a step only where the steps still occupy half the blocks
+// that fit: 512 x 2 rows of 4096 bf16 (gradients) take 4.8 us with one token
+// a step and 7.3 with four, 4096 x 2 rows 34.5 and 32.2, 16384 x 2 rows 160
+// and 116.
+template <typename T, int G, int P>
+bool fills(const MoeArgs& a, bool grad) {
+  const Plan q = plan<T, G, P>(a, grad);
+  return a.top_k <= Step<P>::KK && 2 * q.steps * q.segs >= q.resident;
+}
 template <typename T, int G>
 cudaError_t launch_g(const MoeArgs& a, bool grad, cudaStream_t st) {
-  if (a.top_k <= 2) return launch_gp<T, G, 4>(a, grad, st);
-  if (a.top_k <= 4) return launch_gp<T, G, 2>(a, grad, st);
+  if (fills<T, G, 4>(a, grad)) return launch_gp<T, G, 4>(a, grad, st);
+  if (fills<T, G, 2>(a, grad)) return launch_gp<T, G, 2>(a, grad, st);
   return launch_gp<T, G, 1>(a, grad, st);
 }
 
