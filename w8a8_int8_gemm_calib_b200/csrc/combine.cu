@@ -27,9 +27,10 @@ namespace {
 
 constexpr int kBatch = 8;  // assignments whose rows are in flight together
 
-// A thread's part of a row: U pieces of G bytes (V elements each), the block's
-// threads side by side in each.  G is 16, or what the rows' pitch keeps
-// aligned (4, or a bf16's 2): then four pieces.
+// A thread's part of a row: U pieces of G bytes (V elements each).  G is 16,
+// or what the rows' pitch keeps aligned (4, or a bf16's 2): then four pieces,
+// a warp's 32 lanes side by side in each, so that they are at constant offsets
+// from the first (c) and cost one address.
 template <typename T, int G>
 struct Part {
   static constexpr int V = G / (int)sizeof(T);
@@ -37,17 +38,25 @@ struct Part {
   static constexpr int E = U * V;
   uint32_t w[G == 16 ? 4 : U];
 
-  __device__ __forceinline__ void load(const T* row, const int (&c)[U], int n) {
+  // first column of thread `tid` of a block whose first column is c0
+  static __device__ __forceinline__ int column(int c0, int tid) {
+    return c0 + (tid & ~31) * E + (tid & 31) * V;
+  }
+  // column of element e of a thread whose first is c
+  static __device__ __forceinline__ int column_of(int c, int e) { return c + e / V * 32 * V; }
+
+  __device__ __forceinline__ void load(const T* row, int c, int n) {
+    const T* p = row + c;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (c[u] >= n) continue;
+      if (c + u * 32 * V >= n) continue;
       if constexpr (G == 16) {
-        const uint4 q = ld_stream_u4(row + c[u]);
+        const uint4 q = ld_stream_u4(p);
         w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
       } else if constexpr (G == 4) {
-        w[u] = __ldcg(reinterpret_cast<const unsigned int*>(row + c[u]));
+        w[u] = __ldcg(reinterpret_cast<const unsigned int*>(p + u * 32 * V));
       } else {
-        w[u] = __ldcg(reinterpret_cast<const unsigned short*>(row + c[u]));
+        w[u] = __ldcg(reinterpret_cast<const unsigned short*>(p + u * 32 * V));
       }
     }
   }
@@ -66,7 +75,7 @@ struct Part {
       }
     }
   }
-  static __device__ __forceinline__ void put(T* row, const int (&c)[U], int n, const float (&v)[E]) {
+  static __device__ __forceinline__ void put(T* row, int c, int n, const float (&v)[E]) {
     uint32_t o[G == 16 ? 4 : U];
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -84,15 +93,16 @@ struct Part {
         o[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
+    T* p = row + c;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (c[u] >= n) continue;
+      if (c + u * 32 * V >= n) continue;
       if constexpr (G == 16)
-        *reinterpret_cast<uint4*>(row + c[u]) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
       else if constexpr (G == 4)
-        *reinterpret_cast<uint32_t*>(row + c[u]) = o[u];
+        *reinterpret_cast<uint32_t*>(p + u * 32 * V) = o[u];
       else
-        *reinterpret_cast<uint16_t*>(row + c[u]) = (uint16_t)o[u];
+        *reinterpret_cast<uint16_t*>(p + u * 32 * V) = (uint16_t)o[u];
     }
   }
 };
@@ -132,10 +142,7 @@ __global__ void __launch_bounds__(kRowThreads, kBlocks<P>) combine_kernel(const 
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, n = (int)a.N;
-  int c[L::U];
-#pragma unroll
-  for (int u = 0; u < L::U; ++u)
-    c[u] = ((int)(blockIdx.y * L::U + u) * (int)blockDim.x + (int)threadIdx.x) * L::V;
+  const int c = L::column((int)(blockIdx.y * blockDim.x) * L::E, threadIdx.x);
   const T* z = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.res);
   T* y = static_cast<T*>(a.out);
@@ -236,9 +243,7 @@ __global__ void __launch_bounds__(kRowThreads, kBlocks<P>) combine_grad_kernel(c
       for (int b = 0; b < kBatch; ++b) dot[b] = 0.0f;
       // whole warps run every step (the places are passed by shuffle)
       for (int c0 = 0; c0 < n; c0 += nt * L::E) {  // n <= 2^20
-        int c[L::U];
-#pragma unroll
-        for (int u = 0; u < L::U; ++u) c[u] = c0 + (u * nt + (int)threadIdx.x) * L::V;
+        const int c = L::column(c0, threadIdx.x);
         L dr[P], zr[kBatch];
 #pragma unroll
         for (int p = 0; p < P; ++p)
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kRowThreads, kBlocks<P>) combine_grad_kernel(c
               zr[b].get(v);
 #pragma unroll
               for (int e = 0; e < L::E; ++e)
-                if (c[e / L::V] < n) dot[b] = __fmaf_rn(d[e], v[e], dot[b]);
+                if (L::column_of(c, e) < n) dot[b] = __fmaf_rn(d[e], v[e], dot[b]);
             }
             if (dz && row_ok(a, r, a.R)) {
 #pragma unroll
