@@ -173,12 +173,14 @@ def _here(stream):
 
 
 def _scratch(workspace, need, what):
-    """(pointer, bytes) of a Workspace or a uint8 tensor of at least `need` bytes."""
+    """(pointer, bytes) of a Workspace or a tensor of at least `need` bytes."""
     if not need:
         return None, 0
     if workspace is None:
         raise ValueError(f"{what} needs a workspace of {need} bytes")
     ws = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    if ws.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: the workspace is not on the current CUDA device")
     return _ptr(ws), ws.numel() * ws.element_size()
 
 
@@ -327,17 +329,21 @@ def sq_gemm_workspace_bytes(M, N, K) -> int:
 
 
 class Workspace:
-    """Device scratch for sq_gemm_w8a8, grown on demand.  The GEMM needs no
-    particular contents: each call resets the part it counts with."""
+    """Device scratch for the calls that take a workspace, grown on demand.
+    They need no particular contents.  A buffer that was outgrown is kept: a
+    captured graph may still replay calls that use it."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self._outgrown = []
 
     def get(self, nbytes: int):
         if nbytes == 0:
             return None
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.buf is not None:
+                self._outgrown.append(self.buf)
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
         return self.buf
 

@@ -349,7 +349,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       for (int i = 0; i < C::MY_CHUNKS; ++i) as_w[i * 32 + lane] = as_n[i];
       __syncwarp();
       fetch(tile + units);
-      if (!tc::mbar_wait(tfull_bar(abuf), aphase, abort_flag, kWaitNs, p.status)) break;
+      const bool got = tc::mbar_wait(tfull_bar(abuf), aphase, abort_flag, kWaitNs, p.status);
+      if (!__all_sync(0xffffffffu, got)) break;  // the warp gives up as one
       tc::tc_fence_after();
       const float* as_c = as_w;
       const uint32_t taddr = tmem_base + abuf * TILE_R + ((uint32_t)(quarter * 32) << 16);
