@@ -37,9 +37,6 @@
 #include "tc_ptx.cuh"
 #include "tmaps.h"
 
-#ifndef EPIW
-#define EPIW 8
-#endif
 namespace sq {
 
 namespace {
@@ -48,19 +45,20 @@ constexpr int BK = 128;              // bytes of K per stage: one 128-byte swizz
 constexpr int UK = 32;               // K per tcgen05.mma kind::i8
 constexpr int CH = 128;              // channels per CTA
 constexpr int TILE_N = 2 * CH;       // channels per pair
-constexpr int TILE_R = 256;          // rows per tile, at most
-constexpr int STEP_R = 32;           // and their granularity (MMA N of a CTA pair)
+constexpr int STEP_R = 32;           // granularity of a tile's rows (MMA N of a CTA pair)
 constexpr int W_BYTES = CH * BK;     // a stage's weights
-constexpr int X_BYTES = TILE_R / 2 * BK;  // and rows (at most)
-constexpr int STAGE = W_BYTES + X_BYTES;
 constexpr int BOXES = 4;             // row boxes of 16, 32, 64 and 128
 constexpr uint64_t kWaitNs = 4000000000ull;   // 4 s: far above any pipeline step
 constexpr uint64_t kDrainNs = 1000000000ull;  // waits for copies already in flight
 constexpr uint64_t kPairGraceNs = 2000000ull; // after a time-out: the peer's copies land
-constexpr uint32_t TMEM_COLS = 512;
 
-template <bool BF16, int EPI_W>
+// TILE_R: rows per tile, at most (256, or 32 for a few rows per expert).
+template <bool BF16, int TILE_R>
 struct Cfg {
+  static constexpr int EPI_W = TILE_R > 32 ? 8 : 4;  // epilogue warps
+  static constexpr uint32_t TMEM_COLS = 2 * TILE_R;
+  static constexpr int X_BYTES = TILE_R / 2 * BK;    // a stage's rows, at most
+  static constexpr int STAGE = W_BYTES + X_BYTES;
   static constexpr int THREADS = 64 + 32 * EPI_W;
   static constexpr int EPI_BUF = BF16 ? 32 * 64 : 32 * 128;  // 32 rows x 32 channels
   static constexpr int NB = EPI_W > 4 ? 1 : 2;               // buffers per warp
@@ -68,6 +66,7 @@ struct Cfg {
   static constexpr int MY_CHUNKS = TILE_R / 32 / (EPI_W / 4);  // 32-row chunks a warp drains
   static constexpr int AS_BYTES = EPI_W * MY_CHUNKS * 32 * 4;  // their rows' steps
   static constexpr int TABLE = 2 * (kMaxExperts + 1) * 4;
+  static_assert(MY_CHUNKS >= 1 && STAGE % 1024 == 0, "chunks, swizzle atoms");
   static constexpr int FIXED = 1024 + EPI_BYTES + AS_BYTES + 256 + TABLE;
   static constexpr int STAGES = (227 * 1024 - FIXED) / STAGE;
   static constexpr size_t SMEM = FIXED + (size_t)STAGES * STAGE;
@@ -97,7 +96,7 @@ struct RowMaps {
 // tiles[e], the row tiles before expert e.  Offsets outside [0, R] or falling
 // ones are clamped to a rising sequence, so a bad table gives rows to the
 // wrong expert but touches nothing outside the arrays.
-__device__ __forceinline__ void group_table(const Params& p, int* off, int* tiles) {
+__device__ __forceinline__ void group_table(const Params& p, int tile_r, int* off, int* tiles) {
   const int lane = threadIdx.x & 31;
   int top = 0, before = 0;
   for (int e0 = 0; e0 <= p.E; e0 += 32) {
@@ -111,7 +110,7 @@ __device__ __forceinline__ void group_table(const Params& p, int* off, int* tile
     v = max(v, top);
     const int prev = __shfl_up_sync(0xffffffffu, v, 1);
     // the rows between offsets e - 1 and e are expert e - 1's
-    const int n = e > 0 && e <= p.E ? (v - (lane ? prev : top) + TILE_R - 1) / TILE_R : 0;
+    const int n = e > 0 && e <= p.E ? (v - (lane ? prev : top) + tile_r - 1) / tile_r : 0;
     int s = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -156,17 +155,18 @@ __device__ __forceinline__ void locate(const Params& p, const int* off, const in
   t.mma_n = (t.rows + STEP_R - 1) / STEP_R * STEP_R;
 }
 
-template <bool BF16, int EPI_W>
-__global__ void __launch_bounds__(Cfg<BF16, EPI_W>::THREADS, 1)
+template <bool BF16, int TILE_R>
+__global__ void __launch_bounds__(Cfg<BF16, TILE_R>::THREADS, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ RowMaps tmX,
                const __grid_constant__ CUtensorMap tmY, const Params p) {
-  using C = Cfg<BF16, EPI_W>;
-  constexpr int STAGES = C::STAGES;
+  using C = Cfg<BF16, TILE_R>;
+  constexpr int STAGES = C::STAGES, X_BYTES = C::X_BYTES, EPI_W = C::EPI_W;
+  constexpr uint32_t TMEM_COLS = C::TMEM_COLS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sW = smem;
   uint8_t* sX = smem + STAGES * W_BYTES;
-  uint8_t* sEpi = smem + STAGES * STAGE;  // 1024-aligned
+  uint8_t* sEpi = smem + STAGES * C::STAGE;  // 1024-aligned
   float* sAs = reinterpret_cast<float*>(sEpi + C::EPI_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES + C::AS_BYTES);
   // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], drain
@@ -206,7 +206,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     tc::tmem_relinquish_pair();
   }
   pdl_wait();  // nothing before this touches global memory
-  if (warp == 0) group_table(p, off, tiles);
+  if (warp == 0) group_table(p, TILE_R, off, tiles);
   tc::tc_fence_before();
   tc::cluster_sync();  // the peer's barriers are initialised, this CTA's table is filled
   tc::tc_fence_after();
@@ -471,17 +471,24 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 // Row tiles per raster band: about 32 MB of rows, 4 to 16 tiles, as the plain
 // GEMM's CTA pairs take it.
 int band_tiles(int64_t K) {
-  const int64_t t = ((int64_t)32 << 20) / (TILE_R * K);
+  const int64_t t = ((int64_t)32 << 20) / (256 * K);
   return t > 16 ? 16 : t < 4 ? 4 : (int)t;
 }
 
+// Tiles of 32 rows leave room for 11 stages of weights where 256 rows leave
+// 6, and with few rows the stream of the weights is all there is: with 256 and
+// 32 rows, 8 experts of 4096x4096 with a row each take 25.7 and 24.8 us, of
+// 256x4096 10.7 and 9.9, of 14336x4096 with 32 rows each 82.0 and 78.4.  An
+// expert with more rows reads its weights again from L2.
+bool few_rows(int64_t R, int64_t E) { return R <= 32 * E; }
+
 // The number of pairs that can be resident at once is queried once per
 // device; a persistent launch never asks for more.
-template <bool BF16, int EPI_W>
+template <bool BF16, int TILE_R>
 cudaError_t launch_t(const CUtensorMap& tw, const RowMaps& tx, const CUtensorMap& ty,
                      const Params& p, int64_t most, cudaStream_t st) {
-  using C = Cfg<BF16, EPI_W>;
-  auto kern = grouped_kernel<BF16, EPI_W>;
+  using C = Cfg<BF16, TILE_R>;
+  auto kern = grouped_kernel<BF16, TILE_R>;
   static std::once_flag once[64];
   static cudaError_t err[64];
   static int max_pairs[64];
@@ -547,10 +554,16 @@ sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st) {
   // TMA stores need 16-byte row pitches; other widths store directly
   p.tma_store = (a.N % (bf16 ? 8 : 4)) == 0 &&
                 make_tmap_out(&ty, a.y, (uint64_t)a.N, (uint64_t)a.R, bf16, bf16 ? 64 : 128);
+  const int tile_r = few_rows(a.R, a.E) ? 32 : 256;
   // tiles, whatever the offsets
-  const int64_t most = ((a.R + TILE_R - 1) / TILE_R + a.E) * p.n_tiles;
-  const cudaError_t e = bf16 ? launch_t<true, EPIW>(tw, tx, ty, p, most, st)
-                             : launch_t<false, EPIW>(tw, tx, ty, p, most, st);
+  const int64_t most = ((a.R + tile_r - 1) / tile_r + a.E) * p.n_tiles;
+  cudaError_t e;
+  if (tile_r == 32)
+    e = bf16 ? launch_t<true, 32>(tw, tx, ty, p, most, st)
+             : launch_t<false, 32>(tw, tx, ty, p, most, st);
+  else
+    e = bf16 ? launch_t<true, 256>(tw, tx, ty, p, most, st)
+             : launch_t<false, 256>(tw, tx, ty, p, most, st);
   if (e != cudaSuccess) return fail(SQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   return SQ_OK;
 }
