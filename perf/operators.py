@@ -214,8 +214,7 @@ def _run_own(s, c):
         return [s["offsets"], s["pos"], s["xs"], s["scale_s"]]
     if c["kind"] == "experts":
         sq.sq_gemm_w8a8_grouped(s["xq"], s["wq"], s["offsets"], s["act"], s["ws"], s["y"],
-                                per_token=c["per_token"], bias=s["bias"],
-                                workspace=s["workspace"])
+                                per_token=c["per_token"], bias=s["bias"])
         return s["y"]
     if c["kind"] == "combine":
         return sq.sq_moe_combine(s["z"], s["pos"], s["y"], weights=s["weights"],
