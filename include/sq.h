@@ -385,21 +385,15 @@ sq_status sq_moe_combine_grad(const void* dy, sq_dtype t, int64_t T, int64_t N,
  *   Offsets must be non-decreasing in [0, R]; values that are not are clamped
  *   (rows may then go to another expert, but nothing outside the arrays is
  *   touched).  An expert may have no rows; its weights are then not read.
- *   workspace: at least sq_gemm_w8a8_grouped_workspace_bytes(R,N,K,E) bytes,
- *   16-byte aligned (may be NULL when that is 0); it needs no initialization
- *   and concurrent calls must not share one.
- * K as everywhere; errors as sq_gemm_w8a8; (R / 128 + E) times the 128-column
+ * No workspace.  K as everywhere; errors as sq_gemm_w8a8; (R / 128 + E) times the 128-column
  * tiles of N must stay below 2^31.
  */
-size_t sq_gemm_w8a8_grouped_workspace_bytes(int64_t R, int64_t N, int64_t K,
-                                            int64_t E);
 sq_status sq_gemm_w8a8_grouped(const int8_t* xq, const int8_t* wq,
                                const int32_t* offsets, int64_t R, int64_t N,
                                int64_t K, int64_t E, const float* act_scale,
                                int act_per_token, const float* w_scale,
                                const float* bias, void* y, sq_dtype yt,
-                               int32_t* acc_out, void* workspace,
-                               size_t workspace_bytes, sq_stream stream);
+                               int32_t* acc_out, sq_stream stream);
 
 /*
  * sq_gemm_workspace_bytes -- device scratch sq_gemm_w8a8 needs for this

@@ -111,9 +111,9 @@ def test_moe_combine_grad_checks(lib):
 
 def test_grouped_checks(lib):
     def call(xq=A, wq=A, off=A2, R=8, N=16, K=16, E=4, act=A, pt=1, ws=A, bias=None, y=A, yt=1,
-             acc=None, work=None, n=0):
+             acc=None):
         return lib.lib.sq_gemm_w8a8_grouped(xq, wq, off, R, N, K, E, act, pt, ws, bias, y, yt, acc,
-                                            work, n, None)
+                                            None)
 
     for yt in (2, 3, 4):
         assert call(yt=yt) == lib.SQ_ERR_DTYPE
@@ -125,7 +125,6 @@ def test_grouped_checks(lib):
     for name in ("xq", "wq", "off", "act", "ws", "y", "bias", "acc"):
         assert call(**{name: MIS}) == lib.SQ_ERR_ALIGN
     assert call(R=0) == lib.SQ_OK and call(N=0) == lib.SQ_OK
-    assert lib.lib.sq_gemm_w8a8_grouped_workspace_bytes(0, 16, 16, 4) == 0
 
 
 def test_python_arguments():

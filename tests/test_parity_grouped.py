@@ -57,7 +57,7 @@ def _check(sq, counts, N, K, out, seed=0, per_token=True, bias=True, first=0, sp
     acc = torch.full((R, N), -5, dtype=torch.int32, device="cuda")
     want_y, want_acc = _want(xq, wq, off, act, ws, b, out, y, acc)
     sq.sq_gemm_w8a8_grouped(xq, wq, torch.tensor(off, dtype=torch.int32, device="cuda"), act, ws, y,
-                            per_token=per_token, bias=b, acc_out=acc, workspace=sq.Workspace())
+                            per_token=per_token, bias=b, acc_out=acc)
     sq.sq_sync_status()
     assert torch.equal(acc, want_acc)
     view = torch.int16 if out == torch.bfloat16 else torch.int32
@@ -108,7 +108,7 @@ def test_extreme_codes_and_the_widest_k(sq):
     acc = torch.empty(5, N, dtype=torch.int32, device="cuda")
     y = torch.empty(5, N, device="cuda")
     sq.sq_gemm_w8a8_grouped(xq, wq, off, torch.ones(1, device="cuda"), torch.ones(2, N, device="cuda"),
-                            y, per_token=False, acc_out=acc, workspace=sq.Workspace())
+                            y, per_token=False, acc_out=acc)
     sq.sq_sync_status()
     top = 127 * 127 * K
     assert bool((acc[:2] == top).all()) and bool((acc[2:] == -top).all())
@@ -130,7 +130,7 @@ def test_bad_offsets_stay_inside(sq, rows):
     acc = torch.full((rows + 8, N), -5, dtype=torch.int32, device="cuda")
     want, _ = _want(xq, wq, rise, act, ws, None, torch.float32, y, acc)
     sq.sq_gemm_w8a8_grouped(xq[:rows], wq, torch.tensor(bad, dtype=torch.int32, device="cuda"),
-                            act[:rows], ws, y[:rows], workspace=sq.Workspace())
+                            act[:rows], ws, y[:rows])
     sq.sq_sync_status()
     assert torch.equal(y, want)
 
@@ -144,7 +144,7 @@ def test_against_the_plain_gemm(sq, orc, R, E):
     off = [0, *cut.tolist(), R]
     y = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
     sq.sq_gemm_w8a8_grouped(xq, wq, torch.tensor(off, dtype=torch.int32, device="cuda"), act, ws, y,
-                            bias=b, workspace=sq.Workspace())
+                            bias=b)
     work = sq.Workspace()
     for e in range(E):
         a, z = off[e], off[e + 1]
@@ -174,8 +174,7 @@ def test_weights_past_32_bits(sq):
         y = torch.empty(R, N, device="cuda")
         acc = torch.empty(R, N, dtype=torch.int32, device="cuda")
         sq.sq_gemm_w8a8_grouped(xq, wq, off, torch.ones(R, device="cuda"),
-                                torch.ones(E, N, device="cuda"), y, acc_out=acc,
-                                workspace=sq.Workspace())
+                                torch.ones(E, N, device="cuda"), y, acc_out=acc)
         sq.sq_sync_status()
         assert torch.equal(acc[:, N - 130:], (xq.double() @ wq[E - 1, N - 130:].double().t()).int())
         assert not bool(acc[:, :N - 130].any()) and torch.equal(y, acc.float())
@@ -216,21 +215,18 @@ class _Block:
         self.uq, self.ua = empty(R, N, dtype=torch.int8), empty(R)
         self.z = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
         self.work = sq.Workspace()
-        n = max(sq.sq_moe_sort_workspace_bytes(T, k, E),
-                sq.sq_gemm_w8a8_grouped_workspace_bytes(R, 2 * N, K, E),
-                sq.sq_gemm_w8a8_grouped_workspace_bytes(R, K, N, E))
-        self.work.get(n)
+        self.work.get(sq.sq_moe_sort_workspace_bytes(T, k, E))
 
     def run(self):
         sq = self.sq
         sq.sq_add_rms_smooth_quant_act(self.x, self.res, self.h, self.xq, self.act, self.gamma)
         sq.sq_moe_sort(self.ids, self.E, self.off, self.pos, workspace=self.work)
         sq.sq_moe_gather(self.xq, self.pos, self.xs, scale=self.act, scale_s=self.acts)
-        sq.sq_gemm_w8a8_grouped(self.xs, self.up, self.off, self.acts, self.ups, self.u, workspace=self.work)
+        sq.sq_gemm_w8a8_grouped(self.xs, self.up, self.off, self.acts, self.ups, self.u)
         gate, up = self.u.float().chunk(2, 1)
         self.a = (torch.nn.functional.silu(gate) * up).bfloat16()
         sq.sq_ln_smooth_quant_act(self.a, self.uq, self.ua)
-        sq.sq_gemm_w8a8_grouped(self.uq, self.dn, self.off, self.ua, self.dns, self.z, workspace=self.work)
+        sq.sq_gemm_w8a8_grouped(self.uq, self.dn, self.off, self.ua, self.dns, self.z)
         sq.sq_moe_combine(self.z, self.pos, self.y, weights=self.wts, residual=self.h)
         return self.y
 

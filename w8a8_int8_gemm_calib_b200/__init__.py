@@ -32,7 +32,7 @@ __all__ = [
     "sq_debug_bounds_enabled", "sq_selftest_bounds_check",
     "sq_add_rms_smooth_quant_act", "sq_moe_sort_workspace_bytes", "sq_moe_sort",
     "sq_moe_gather", "sq_moe_combine", "sq_moe_combine_grad",
-    "sq_gemm_w8a8_grouped_workspace_bytes", "sq_gemm_w8a8_grouped",
+    "sq_gemm_w8a8_grouped",
 ]
 
 
@@ -373,29 +373,22 @@ def sq_gemm_w8a8(xq, wq, act_scale, w_scale, y, per_token=True, acc_out=None,
     return y
 
 
-def sq_gemm_w8a8_grouped_workspace_bytes(R, N, K, E) -> int:
-    return int(lib.sq_gemm_w8a8_grouped_workspace_bytes(R, N, K, E))
-
-
 def sq_gemm_w8a8_grouped(xq, wq, offsets, act_scale, w_scale, y, per_token=True, bias=None,
-                         acc_out=None, workspace=None, stream=None):
+                         acc_out=None, stream=None):
     """The experts' GEMM: rows offsets[e] .. offsets[e + 1] - 1 of xq [R, K]
     with wq[e] of [E, N, K], dequantized by act_scale and w_scale [E, N] (+
     bias [E, N]); y [R, N] fp32 or bf16."""
     R, K = xq.shape
-    E, N, _ = wq.shape
-    ws, nbytes = _scratch(workspace, sq_gemm_w8a8_grouped_workspace_bytes(R, N, K, E),
-                          "sq_gemm_w8a8_grouped")
+    E, N = wq.shape[:2]
+    f32 = torch.float32
     dev, st = _here(stream)
-    check(lib.sq_gemm_w8a8_grouped(_arg(xq, "xq", torch.int8, R * K, dev),
-                                   _arg(wq, "wq", torch.int8, E * N * K, dev),
-                                   _arg(offsets, "offsets", torch.int32, E + 1, dev), R, N, K, E,
-                                   _arg(act_scale, "act_scale", torch.float32, R if per_token else 1, dev),
-                                   int(per_token), _arg(w_scale, "w_scale", torch.float32, E * N, dev),
-                                   _arg(bias, "bias", torch.float32, E * N, dev),
-                                   _arg(y, "y", y.dtype, R * N, dev), _dt(y),
-                                   _arg(acc_out, "acc_out", torch.int32, R * N, dev), ws, nbytes,
-                                   st), "sq_gemm_w8a8_grouped")
+    check(lib.sq_gemm_w8a8_grouped(
+        _arg(xq, "xq", torch.int8, R * K, dev), _arg(wq, "wq", torch.int8, E * N * K, dev),
+        _arg(offsets, "offsets", torch.int32, E + 1, dev), R, N, K, E,
+        _arg(act_scale, "act_scale", f32, R if per_token else 1, dev), int(per_token),
+        _arg(w_scale, "w_scale", f32, E * N, dev), _arg(bias, "bias", f32, E * N, dev),
+        _arg(y, "y", y.dtype, R * N, dev), _dt(y), _arg(acc_out, "acc_out", torch.int32, R * N, dev),
+        st), "sq_gemm_w8a8_grouped")
     return y
 
 

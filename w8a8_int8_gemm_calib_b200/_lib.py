@@ -47,7 +47,7 @@ EXPORTS = [
     "sq_debug_bounds_enabled", "sq_selftest_bounds_check",
     "sq_add_rms_smooth_quant_act", "sq_moe_sort_workspace_bytes", "sq_moe_sort",
     "sq_moe_gather", "sq_moe_combine", "sq_moe_combine_grad",
-    "sq_gemm_w8a8_grouped_workspace_bytes", "sq_gemm_w8a8_grouped",
+    "sq_gemm_w8a8_grouped",
 ]
 
 
@@ -101,9 +101,7 @@ def _load() -> ctypes.CDLL:
     L.sq_moe_gather.argtypes = [p, i, i64, i64, p, p, i64, i64, p, p, p]
     L.sq_moe_combine.argtypes = [p, i, i64, i64, p, p, i64, i64, p, p, p]
     L.sq_moe_combine_grad.argtypes = [p, i, i64, i64, p, p, i64, p, i64, p, p, p]
-    L.sq_gemm_w8a8_grouped_workspace_bytes.argtypes = [i64, i64, i64, i64]
-    L.sq_gemm_w8a8_grouped_workspace_bytes.restype = sz
-    L.sq_gemm_w8a8_grouped.argtypes = [p, p, p, i64, i64, i64, i64, p, i, p, p, p, i, p, p, sz, p]
+    L.sq_gemm_w8a8_grouped.argtypes = [p, p, p, i64, i64, i64, i64, p, i, p, p, p, i, p, p]
     for fn in ("sq_calib_absmax", "sq_smooth_scales", "sq_fuse_weights_q8",
                "sq_ln_smooth_quant_act", "sq_gemm_w8a8", "sq_sync_status",
                "sq_selftest_bounded_wait", "sq_gemm_w8a8_noalloc", "sq_gemm_w8a8_bias",

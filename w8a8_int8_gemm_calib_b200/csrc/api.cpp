@@ -455,16 +455,10 @@ sq_status sq_moe_combine_grad(const void* dy, sq_dtype t, int64_t T, int64_t N, 
   return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
 }
 
-size_t sq_gemm_w8a8_grouped_workspace_bytes(int64_t R, int64_t N, int64_t K, int64_t E) {
-  if (R <= 0 || N <= 0 || K <= 0 || E <= 0) return 0;
-  return gemm_grouped_workspace_bytes(R, N, K, E);
-}
-
 sq_status sq_gemm_w8a8_grouped(const int8_t* xq, const int8_t* wq, const int32_t* offsets,
                                int64_t R, int64_t N, int64_t K, int64_t E, const float* act_scale,
                                int act_per_token, const float* w_scale, const float* bias, void* y,
-                               sq_dtype yt, int32_t* acc_out, void* workspace,
-                               size_t workspace_bytes, sq_stream stream) {
+                               sq_dtype yt, int32_t* acc_out, sq_stream stream) {
   const char* fn = "sq_gemm_w8a8_grouped";
   g_last_error[0] = 0;
   SQ_TRY(check_dtype(yt, fn));
@@ -483,18 +477,10 @@ sq_status sq_gemm_w8a8_grouped(const int8_t* xq, const int8_t* wq, const int32_t
   SQ_OPT(bias, fn);
   SQ_REQ(y, fn);
   SQ_OPT(acc_out, fn);
-  const size_t need = gemm_grouped_workspace_bytes(R, N, K, E);
-  if (need) {
-    if (!workspace || workspace_bytes < need)
-      return fail(SQ_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
-                  workspace ? workspace_bytes : (size_t)0);
-    SQ_OPT(workspace, fn);
-  }
   GroupArgs a{};
   a.xq = xq; a.wq = wq; a.offsets = offsets; a.R = R; a.N = N; a.K = K; a.E = E;
   a.act_scale = act_scale; a.act_per_token = act_per_token ? 1 : 0;
   a.w_scale = w_scale; a.bias = bias; a.y = y; a.yt = yt; a.acc_out = acc_out;
-  a.workspace = workspace;
   return launch_gemm_grouped(a, (cudaStream_t)stream);
 }
 

@@ -12,11 +12,11 @@
 // any multiple of 32.  So an expert with 300 rows computes 320 (two tiles of
 // 160), where 256-row tiles would compute 512: rows per expert are ragged,
 // channels are not.  The weights then stream through the A operand once per
-// 256 rows whatever the number of rows is.
+// 256 rows (32, where the experts have few) whatever the number of rows is.
 //
 // Persistent CTA pairs (tcgen05 cta_group::2, one pair per two SMs): each CTA
 // loads 128 channels of weights and half the tile's rows per 128-byte k-block
-// (16 KB + up to 16 KB), the even CTA issues the MMAs for both, each CTA
+// (16 KB + up to 16 KB; 2 KB with 32-row tiles), the even CTA issues the MMAs for both, each CTA
 // drains its 128 channels.  Two accumulators of 256 TMEM columns, so one
 // tile's epilogue runs under the next tile's main loop.  Warp 0 issues the
 // loads, warp 1 the MMAs, the others drain.  Every wait is bounded.
@@ -523,8 +523,6 @@ cudaError_t launch_t(const CUtensorMap& tw, const RowMaps& tx, const CUtensorMap
 }
 
 }  // namespace
-
-size_t gemm_grouped_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
 
 sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st) {
   const char* fn = "sq_gemm_w8a8_grouped";

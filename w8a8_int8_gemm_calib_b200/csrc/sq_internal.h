@@ -189,9 +189,7 @@ struct GroupArgs {
   void* y;
   sq_dtype yt;
   int32_t* acc_out;
-  void* workspace;
 };
-size_t gemm_grouped_workspace_bytes(int64_t R, int64_t N, int64_t K, int64_t E);
 sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st);
 
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
