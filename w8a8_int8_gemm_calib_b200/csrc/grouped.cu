@@ -84,6 +84,7 @@ struct Params {
   const float* bias;
   void* y;
   int tma_store;
+  int piece;  // bytes that the rows' pitch keeps aligned: 16, 8, 4, or a bf16's 2
   int32_t* acc;
   unsigned int* status;
 };
@@ -153,6 +154,46 @@ __device__ __forceinline__ void locate(const Params& p, const int* off, const in
   t.row0 = off[t.e] + mb * per;
   t.rows = min(per, all - mb * per);
   t.mma_n = (t.rows + STEP_R - 1) / STEP_R * STEP_R;
+}
+
+// Rows row0 .. row0 + valid - 1, channels col0 .. col0 + 31, from a swizzled
+// buffer in pieces of G bytes (G divides the rows' pitch), several rows a step.
+template <int G> struct Piece;
+template <> struct Piece<16> { using T = uint4; };
+template <> struct Piece<8> { using T = uint2; };
+template <> struct Piece<4> { using T = uint32_t; };
+template <> struct Piece<2> { using T = uint16_t; };
+template <bool BF16, int G>
+__device__ __forceinline__ void store_rows(const Params& p, const uint8_t* buf, int row0, int valid,
+                                           int col0, int lane) {
+  if constexpr (BF16 || G > 2) {
+    using T = typename Piece<G>::T;
+    constexpr int ES = BF16 ? 2 : 4, ROW = 32 * ES;  // a row's bytes in the buffer
+    constexpr int LANES = ROW / G;                   // lanes on a row
+    constexpr int ROWS = 32 / LANES;                 // rows a step
+    constexpr int STEPS = 32 / ROWS, U = 4;  // STEPS is 4, 8, 16 or 32
+    const int off = lane % LANES * G, n = col0 + off / ES;
+    if (n >= p.N) return;
+    const int64_t first = (int64_t)(row0 + lane / LANES) * p.N + n, step = (int64_t)ROWS * p.N;
+    uint8_t* y = static_cast<uint8_t*>(p.y) + first * ES;
+#pragma unroll 1
+    for (int s0 = 0; s0 < STEPS && s0 * ROWS < valid; s0 += U) {
+      T v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = (s0 + u) * ROWS + lane / LANES;
+        const int k = (off >> 4) ^ (BF16 ? (i >> 1) & 3 : i & 7);
+        v[u] = *reinterpret_cast<const T*>(buf + i * ROW + k * 16 + (off & 15));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if ((s0 + u) * ROWS + lane / LANES < valid &&
+            in_bounds(first + (s0 + u) * step, G / ES, (int64_t)p.R * p.N, p.status))
+          *reinterpret_cast<T*>(y) = v[u];
+        y += step * ES;
+      }
+    }
+  }
 }
 
 template <bool BF16, int TILE_R>
@@ -429,21 +470,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           continue;
         }
         // A TMA store clips at the tensor's edge, not at the expert's, and
-        // needs 16-byte row pitches: otherwise the rows are written from the
-        // buffer, a row per step.
+        // needs 16-byte row pitches: otherwise the rows go from the buffer in
+        // the pieces their pitch keeps aligned.
         __syncwarp();
-        const int n = col0 + lane;
-        if (n < p.N) {
-          for (int i = 0; i < valid; ++i) {
-            const int64_t o = (int64_t)(row0 + i) * p.N + n;
-            if (!in_bounds(o, 1, (int64_t)p.R * p.N, p.status)) continue;
-            if (BF16)
-              reinterpret_cast<uint16_t*>(p.y)[o] = *reinterpret_cast<const uint16_t*>(
-                  buf + i * 64 + ((lane >> 3) ^ ((i >> 1) & 3)) * 16 + (lane & 7) * 2);
-            else
-              reinterpret_cast<float*>(p.y)[o] = *reinterpret_cast<const float*>(
-                  buf + i * 128 + ((lane >> 2) ^ (i & 7)) * 16 + (lane & 3) * 4);
-          }
+        switch (p.piece) {
+          case 16: store_rows<BF16, 16>(p, buf, row0, valid, col0, lane); break;
+          case 8: store_rows<BF16, 8>(p, buf, row0, valid, col0, lane); break;
+          case 4: store_rows<BF16, 4>(p, buf, row0, valid, col0, lane); break;
+          default: store_rows<BF16, 2>(p, buf, row0, valid, col0, lane); break;
         }
         __syncwarp();  // read before the next chunk overwrites it
       }
@@ -480,7 +514,7 @@ int band_tiles(int64_t K) {
 // 32 rows, 8 experts of 4096x4096 with a row each take 25.7 and 24.8 us, of
 // 256x4096 10.7 and 9.9, of 14336x4096 with 32 rows each 82.0 and 78.4.  An
 // expert with more rows reads its weights again from L2.
-bool few_rows(int64_t R, int64_t E) { return R <= 32 * E; }
+int tile_rows(int64_t R, int64_t E) { return R <= 32 * E ? 32 : 256; }
 
 // The number of pairs that can be resident at once is queried once per
 // device; a persistent launch never asks for more.
@@ -552,7 +586,9 @@ sq_status launch_gemm_grouped(const GroupArgs& a, cudaStream_t st) {
   // TMA stores need 16-byte row pitches; other widths store directly
   p.tma_store = (a.N % (bf16 ? 8 : 4)) == 0 &&
                 make_tmap_out(&ty, a.y, (uint64_t)a.N, (uint64_t)a.R, bf16, bf16 ? 64 : 128);
-  const int tile_r = few_rows(a.R, a.E) ? 32 : 256;
+  const int64_t pitch = a.N * (bf16 ? 2 : 4);
+  p.piece = pitch % 16 == 0 ? 16 : pitch % 8 == 0 ? 8 : pitch % 4 == 0 ? 4 : 2;
+  const int tile_r = tile_rows(a.R, a.E);
   // tiles, whatever the offsets
   const int64_t most = ((a.R + tile_r - 1) / tile_r + a.E) * p.n_tiles;
   cudaError_t e;

@@ -153,17 +153,32 @@ __global__ void __launch_bounds__(32 * W) sort_place_kernel(const SortArgs a) {
     }
     __syncthreads();
   }
-  // the runs' starts within the block, a warp per expert
-  for (int e = warp; e < a.E; e += W) {
-    const int v = lane < W ? cnt[lane * (a.E + 1) + e] : 0;
-    int s = v;
+  // the runs' starts within the block: of 8 runs a thread per expert adds
+  // them up, of 32 a warp
+  if constexpr (W == 8) {
+    for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
+      int s = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
+      for (int w = 0; w < W; ++w) {
+        const int v = cnt[w * (a.E + 1) + e];
+        cnt[w * (a.E + 1) + e] = s;
+        s += v;
+      }
+      if (a.blocks == 1) total[e] = s;
     }
-    if (lane < W) cnt[lane * (a.E + 1) + e] = s - v;
-    if (a.blocks == 1 && lane == 31) total[e] = s;
+  } else {
+    static_assert(W == 32, "a lane per run");
+    for (int e = warp; e < a.E; e += W) {
+      const int v = cnt[lane * (a.E + 1) + e];
+      int s = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+      }
+      cnt[lane * (a.E + 1) + e] = s - v;
+      if (a.blocks == 1 && lane == 31) total[e] = s;
+    }
   }
   __syncthreads();
   // exclusive sums of the totals are the offsets; with the blocks before
