@@ -385,8 +385,8 @@ sq_status sq_moe_combine_grad(const void* dy, sq_dtype t, int64_t T, int64_t N,
  *   Offsets must be non-decreasing in [0, R]; values that are not are clamped
  *   (rows may then go to another expert, but nothing outside the arrays is
  *   touched).  An expert may have no rows; its weights are then not read.
- * No workspace.  K as everywhere; errors as sq_gemm_w8a8; (R / 128 + E) times the 128-column
- * tiles of N must stay below 2^31.
+ * No workspace.  K as everywhere; R and N at most 2^30, and (R / 128 + E)
+ * times the 128-column tiles of N below 2^31; errors as sq_gemm_w8a8.
  */
 sq_status sq_gemm_w8a8_grouped(const int8_t* xq, const int8_t* wq,
                                const int32_t* offsets, int64_t R, int64_t N,

@@ -118,7 +118,8 @@ def test_grouped_checks(lib):
     for yt in (2, 3, 4):
         assert call(yt=yt) == lib.SQ_ERR_DTYPE
     for bad in (dict(R=-1), dict(N=-1), dict(K=0), dict(K=24), dict(K=133152), dict(E=0),
-                dict(E=1025), dict(R=1 << 31), dict(N=1 << 31), dict(R=(1 << 31) - 1, N=1 << 20)):
+                dict(E=1025), dict(R=(1 << 30) + 1), dict(N=(1 << 30) + 1),
+                dict(R=1 << 30, N=1 << 20)):
         assert call(**bad) == lib.SQ_ERR_SHAPE, bad
     for name in ("xq", "wq", "off", "act", "ws", "y"):
         assert call(**{name: None}) == lib.SQ_ERR_INVALID_ARG

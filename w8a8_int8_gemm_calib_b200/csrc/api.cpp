@@ -334,6 +334,7 @@ sq_status sq_add_rms_smooth_quant_act(const void* x, const void* residual, sq_dt
 namespace {
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxWidth = (int64_t)1 << 20;
+constexpr int64_t kMaxCoord = (int64_t)1 << 30;
 
 sq_status check_experts(int64_t E, const char* fn) {
   if (E < 1 || E > kMaxExperts)
@@ -467,8 +468,11 @@ sq_status sq_gemm_w8a8_grouped(const int8_t* xq, const int8_t* wq, const int32_t
   SQ_TRY(check_k(K, fn));
   SQ_TRY(check_experts(E, fn));
   if (R == 0 || N == 0) return SQ_OK;
-  if (R > kMaxRows || N > kMaxRows || (R / 128 + E) > kMaxRows / ((N + 127) / 128))
-    return fail(SQ_ERR_SHAPE, "%s: (R / 128 + E) x (N / 128) tiles must stay below 2^31", fn);
+  // the kernel's row and channel coordinates run past R and N by a tile
+  if (R > kMaxCoord || N > kMaxCoord || (R / 128 + E) > kMaxRows / ((N + 127) / 128))
+    return fail(SQ_ERR_SHAPE,
+                "%s: R and N must not exceed 2^30, and (R / 128 + E) x (N / 128) must stay below 2^31",
+                fn);
   SQ_REQ(xq, fn);
   SQ_REQ(wq, fn);
   SQ_REQ(offsets, fn);

@@ -11,7 +11,9 @@
 // anywhere, so what counts is bytes in flight: a thread has eight 16-byte
 // loads outstanding, of one token's rows or, with few rows a token, of
 // several tokens', and the places of the next step are loaded before the
-// rows of this one.
+// rows of this one.  Measured (bf16 rows of 4096): 16384 tokens of 8 rows, with
+// a residual, 200 us (6.7 TB/s), of 2 rows 86 us; the gradients of 8192 tokens
+// of 8 rows 200 us (5.7 TB/s, half of it writes).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -15,8 +15,8 @@
 #include <stdint.h>
 
 #include "launch.cuh"
-#include "sq_device.cuh"
 #include "moe.cuh"
+#include "sq_device.cuh"
 #include "sq_internal.h"
 
 namespace sq {
@@ -33,7 +33,9 @@ namespace {
 //
 // W warps per block: 32 when there is work for them and their counts fit
 // (E <= 256), else 8.  A warp takes 64 / W steps of 32 assignments at once,
-// so one block holds 2048 either way.
+// so one block holds 2048 either way.  32 assignments over 8 experts take
+// 2.3 us with 8 warps and 3.2 with 32, 16384 over 64 experts 9.2 and 7.2;
+// 131072 over 64 experts take 7.8 us.
 constexpr int kSortItems = 2048;
 constexpr int kSortWide = 256;   // experts
 constexpr int kSortFew = 512;    // assignments that 8 warps place as fast
@@ -258,7 +260,8 @@ cudaError_t launch_sort_t(SortArgs a, cudaStream_t st) {
 // ---------------------------------------------------------------- gather
 // U: the unit a row is copied in.  A block is blockDim.x units of blockDim.y
 // tokens' rows: short rows share a block (16384 x 2 rows of 1024 bytes take
-// 18 us with a block each).
+// 9.6 us, with a block each 18).  16384 x 8 rows of 4096 codes take 99 us, 6.1
+// TB/s of the 604 MB.
 template <typename U>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(const MoeArgs a) {
   pdl_launch_dependents();
