@@ -67,12 +67,12 @@ def _check(sq, counts, N, K, out, seed=0, per_token=True, bias=True, first=0, sp
 OUT = [torch.bfloat16, torch.float32]
 GROUPS = [
     [1], [0, 1], [1, 0, 0, 2], [127, 128, 129], [5, 0, 300, 1, 64, 33], [0, 0, 0], [1000], [7] * 9,
-    [1] * 40, [16, 17, 31, 32, 33, 63, 64, 65, 8, 9], [260, 0, 511, 513], [3] + [0] * 62 + [200],
+    [1] * 40, [16, 17, 31, 32, 33, 63, 64, 65, 8, 9], [260, 0, 511, 513], [3] + [0] * 62 + [200], [4700, 3],
 ]
 
 
 @pytest.mark.parametrize("counts", GROUPS, ids=lambda c: "-".join(map(str, c[:6])) + f"x{len(c)}")
-@pytest.mark.parametrize("N,K", [(256, 128), (17, 48), (1000, 2064), (520, 16), (264, 640)])
+@pytest.mark.parametrize("N,K", [(256, 128), (17, 48), (1000, 2064), (520, 16), (264, 640), (1, 32), (602, 272)])
 @pytest.mark.parametrize("out", OUT, ids=["bf16", "f32"])
 def test_grouped(sq, counts, N, K, out):
     _check(sq, counts, N, K, out, seed=sum(counts) + N + K)
