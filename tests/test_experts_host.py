@@ -35,6 +35,7 @@ def test_add_rms_checks(lib):
     assert "sq_add_rms_smooth_quant_act" in lib.last_error()
     for gran in (0, 1, 2):
         assert call(T=0, gran=gran) == lib.SQ_OK
+        assert call(T=0, gran=gran, x=None, res=None, h=None, xq=None) == lib.SQ_OK
 
 
 def test_moe_sort_checks(lib):

@@ -290,6 +290,31 @@ def test_routed_block_captured_and_on_another_stream(sq, T):
     assert torch.equal(b.y, replayed) and not torch.equal(first, replayed)
 
 
+def test_no_tokens(sq):
+    """An empty batch through every call: nothing is written but offsets."""
+    K, N, E, k = 256, 128, 8, 2
+
+    def empty(*s, dtype=torch.bfloat16):
+        return torch.empty(*s, dtype=dtype, device="cuda")
+
+    x, act = empty(0, K), empty(0, dtype=torch.float32)
+    xq, pos = empty(0, K, dtype=torch.int8), empty(0, k, dtype=torch.int32)
+    off = torch.full((E + 1,), 5, dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(per_token=False), dict(per_tensor_dynamic=True)):
+        step = torch.full((1,), 0.5, device="cuda") if kw else act
+        sq.sq_add_rms_smooth_quant_act(x, x, x, xq, step, torch.ones(K, device="cuda"), **kw)
+        assert not kw or float(step) == 0.5
+    sq.sq_moe_sort(empty(0, k, dtype=torch.int64), E, off, pos)
+    sq.sq_moe_gather(xq, pos, xq, scale=act, scale_s=act)
+    sq.sq_gemm_w8a8_grouped(xq, torch.ones(E, N, K, dtype=torch.int8, device="cuda"), off, act,
+                            torch.ones(E, N, device="cuda"), empty(0, N))
+    z = empty(0, N)
+    sq.sq_moe_combine(z, pos, z)
+    sq.sq_moe_combine_grad(z, pos, z=z, dz=z, dweights=empty(0, k, dtype=torch.float32))
+    sq.sq_sync_status()
+    assert off.tolist() == [0] * (E + 1)
+
+
 def test_two_blocks_at_once(sq):
     """Two calls on two streams, each with its own workspace."""
     blocks = [_Block(sq, T, 256, 128, 16, 2, seed=T) for T in (9, 600)]

@@ -299,6 +299,9 @@ sq_status sq_add_rms_smooth_quant_act(const void* x, const void* residual, sq_dt
     return fail(SQ_ERR_INVALID_ARG, "%s: unknown granularity %d", fn, (int)gran);
   if (T < 0) return fail(SQ_ERR_SHAPE, "%s: T=%lld < 0", fn, (long long)T);
   SQ_TRY(check_k(K, fn));
+  if (!(eps >= 0.0f && isfinite(eps)))
+    return fail(SQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  if (T == 0) return SQ_OK;
   SQ_REQ(x, fn);
   SQ_REQ(residual, fn);
   SQ_REQ(gamma_s, fn);
@@ -307,9 +310,6 @@ sq_status sq_add_rms_smooth_quant_act(const void* x, const void* residual, sq_dt
   SQ_REQ(xq, fn);
   if (n_clipped && (((uintptr_t)n_clipped) & 7u))
     return fail(SQ_ERR_ALIGN, "%s: n_clipped is not 8-byte aligned", fn);
-  if (!(eps >= 0.0f && isfinite(eps)))
-    return fail(SQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
-  if (T == 0) return SQ_OK;
   const cudaStream_t st = (cudaStream_t)stream;
   AddNormArgs a{};
   a.x = x; a.res = residual; a.h = h; a.T = T; a.K = K; a.g = gamma_s; a.eps = eps;
