@@ -290,8 +290,9 @@ sq_status sq_add_rms_smooth_quant_act(const void* x, const void* residual,
  *   offsets [E+1] int32: expert e's rows are offsets[e] .. offsets[e+1] - 1.
  *   pos [T, top_k] int32: the sorted row of each assignment, or -1.
  * Both stay on the device; no call reads them on the host.  T * top_k and the
- * row counts R must be below 2^31, E in [1, 1024], top_k >= 1, a row's width
- * (K or N) in [1, 2^20].  Any other value is SQ_ERR_SHAPE.
+ * row counts R must be below 2^31, E in [1, 1024], top_k >= 1 (for
+ * sq_moe_combine and sq_moe_combine_grad at most 2^30), a row's width (K or N)
+ * in [1, 2^20].  Any other value is SQ_ERR_SHAPE.
  */
 
 /*

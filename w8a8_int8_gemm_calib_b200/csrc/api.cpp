@@ -347,6 +347,13 @@ sq_status check_routing(int64_t T, int64_t top_k, const char* fn) {
                 fn, (long long)T, (long long)top_k);
   return SQ_OK;
 }
+// The combine and its gradient step over a token's choices in 32-bit counters,
+// up to eight past the last one.
+sq_status check_choices(int64_t top_k, const char* fn) {
+  if (top_k > kMaxCoord)
+    return fail(SQ_ERR_SHAPE, "%s: top_k=%lld must not exceed 2^30", fn, (long long)top_k);
+  return SQ_OK;
+}
 sq_status check_rows(int64_t R, int64_t width, const char* fn) {
   if (R < 0 || R > kMaxRows)
     return fail(SQ_ERR_SHAPE, "%s: R=%lld must lie in [0, 2^31)", fn, (long long)R);
@@ -419,6 +426,7 @@ sq_status sq_moe_combine(const void* z, sq_dtype t, int64_t R, int64_t N, const 
   g_last_error[0] = 0;
   SQ_TRY(check_dtype(t, fn));
   SQ_TRY(check_routing(T, top_k, fn));
+  SQ_TRY(check_choices(top_k, fn));
   SQ_TRY(check_rows(R, N, fn));
   if (T == 0) return SQ_OK;
   if (R > 0) SQ_REQ(z, fn);
@@ -440,6 +448,7 @@ sq_status sq_moe_combine_grad(const void* dy, sq_dtype t, int64_t T, int64_t N, 
   g_last_error[0] = 0;
   SQ_TRY(check_dtype(t, fn));
   SQ_TRY(check_routing(T, top_k, fn));
+  SQ_TRY(check_choices(top_k, fn));
   SQ_TRY(check_rows(R, N, fn));
   if (T == 0 || (!dz && !dw)) return SQ_OK;
   SQ_REQ(dy, fn);
