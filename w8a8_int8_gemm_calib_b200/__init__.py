@@ -331,7 +331,8 @@ def sq_gemm_workspace_bytes(M, N, K) -> int:
 class Workspace:
     """Device scratch for the calls that take a workspace, grown on demand.
     They need no particular contents.  A buffer that was outgrown is kept: a
-    captured graph may still replay calls that use it."""
+    captured graph may still replay calls that use it.  Each is at least twice
+    the one before, so all that are kept are smaller than the one in use."""
 
     def __init__(self, device=None):
         self.device = device
@@ -344,6 +345,7 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             if self.buf is not None:
                 self._outgrown.append(self.buf)
+                nbytes = max(nbytes, 2 * self.buf.numel())
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
         return self.buf
 
