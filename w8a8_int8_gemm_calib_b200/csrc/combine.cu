@@ -115,8 +115,9 @@ __device__ __forceinline__ bool row_ok(const MoeArgs& a, int64_t row, int64_t ro
 }
 
 // P tokens a step, their first kBatch / P assignments each: P may be 4 for
-// top_k up to 2, 2 up to 4, else it is 1, with as many steps of 8 as top_k takes.  Lane b
-// of every warp holds the place and weight of the step's assignment b.
+// top_k up to 2, 2 up to 4, else it is 1, with as many steps of 8 as top_k
+// takes.  Lane b of every warp holds the place and weight of the step's
+// assignment b.
 template <int P>
 struct Step {
   static constexpr int KK = kBatch / P;
@@ -132,8 +133,9 @@ struct Step {
 };
 
 // Resident blocks per SM (registers: 64 a thread, 80 with several tokens a
-// step).  16384 x 8 rows of 4096 bf16 are combined in 246 / 221 / 246 us with
-// 3 / 4 / 5 blocks, the gradients of 8192 x 8 rows take 217 / 211 / 300 us.
+// step).  16384 x 8 rows of 4096 bf16 are combined in 230 / 204 / 277 us with
+// 3 / 4 / 5 blocks; the gradients of 8192 x 8 rows take 194 / 201 / 217 us, of
+// 1024 x 4 17.7 us with 3 and 15.4 with 4.
 template <int P>
 constexpr int kBlocks = P == 1 ? 4 : 3;
 
@@ -299,11 +301,12 @@ __global__ void __launch_bounds__(kRowThreads, kBlocks<P>) combine_grad_kernel(c
   }
 }
 
-// Threads per block, blocks across a row, blocks that are resident at once
-// and steps over the tokens, for P tokens a step.
+// Threads per block, blocks across a row, blocks that are resident at once,
+// those of them that walk the tokens side by side and the steps over the
+// tokens, for P tokens a step.
 struct Plan {
   unsigned nt;
-  int64_t segs, resident, steps;
+  int64_t segs, resident, walk, steps;
 };
 template <typename T, int G, int P>
 Plan plan(const MoeArgs& a, bool grad) {
@@ -312,6 +315,7 @@ Plan plan(const MoeArgs& a, bool grad) {
   q.nt = row_threads(pieces);
   q.segs = grad ? 1 : (pieces + q.nt - 1) / q.nt;
   q.resident = kBlocks<P> * (int64_t)sm_count() * (kRowThreads / q.nt);
+  q.walk = (q.resident + q.segs - 1) / q.segs;
   q.steps = (a.T + P - 1) / P;
   return q;
 }
@@ -319,26 +323,46 @@ Plan plan(const MoeArgs& a, bool grad) {
 template <typename T, int G, int P>
 cudaError_t launch_gp(const MoeArgs& a, bool grad, cudaStream_t st) {
   const Plan q = plan<T, G, P>(a, grad);
-  int64_t walk = (q.resident + q.segs - 1) / q.segs;
-  if (walk > q.steps) walk = q.steps;
-  const dim3 grid((unsigned)walk, (unsigned)q.segs);
+  const dim3 grid((unsigned)(q.walk < q.steps ? q.walk : q.steps), (unsigned)q.segs);
   return grad ? launch_pdl(combine_grad_kernel<T, G, P>, grid, dim3(q.nt), 0, st, a)
               : launch_pdl(combine_kernel<T, G, P>, grid, dim3(q.nt), 0, st, a);
 }
 
-// Several tokens a step only where the steps still occupy half the blocks
-// that fit: 512 x 2 rows of 4096 bf16 (gradients) take 4.8 us with one token
-// a step and 7.3 with four, 4096 x 2 rows 34.5 and 32.2, 16384 x 2 rows 160
-// and 116.
+// Four tokens a step (top_k up to 2) where the steps still occupy half the
+// blocks that fit.  us with 1 / 2 / 4 tokens a step, rows of 4096 bf16:
+//   combine    512 x 2: 5.0 / 4.9 / 4.2    1024 x 1: 9.3 / 8.3 / 7.6
+//              8192 x 2: 62.5 / 53.1 / 46.7
+//   gradients  512 x 2: 5.1 / 5.8 / 7.7    1024 x 2: 11.1 / 12.5 / 10.7
+//              8192 x 2: 65.8 / 60.2 / 59.0
+// (512 x 2 is 128 steps for 444 blocks; the combine has two blocks on a row.)
+//
+// Else two (top_k up to 4) where the blocks then walk fewer rounds over the
+// tokens, the gradients of 4 choices only where that is a single round.  us
+// with 1 / 2 tokens a step, 4 choices:
+//   combine    512: 6.6 / 7.4 (2 rounds both)   768: 10.0 / 9.6 (3 and 2)
+//              8192: 73.9 / 66.9
+//   gradients  512: 8.8 / 10.0 (1 both)   768: 13.8 / 12.2 (2 and 1)   1024:
+//              15.4 / 18.4 (2 both)   8192: 96.5 / 104.7 (14 and 10); of 3
+//              choices 8192: 80.3 / 77.1
 template <typename T, int G, int P>
-bool fills(const MoeArgs& a, bool grad) {
+bool fills_half(const MoeArgs& a, bool grad) {
   const Plan q = plan<T, G, P>(a, grad);
-  return a.top_k <= Step<P>::KK && 2 * q.steps * q.segs >= q.resident;
+  return 2 * q.steps * q.segs >= q.resident;
+}
+template <typename T, int G, int P>
+int64_t rounds(const MoeArgs& a, bool grad) {
+  const Plan q = plan<T, G, P>(a, grad);
+  return (q.steps + q.walk - 1) / q.walk;
 }
 template <typename T, int G>
 cudaError_t launch_g(const MoeArgs& a, bool grad, cudaStream_t st) {
-  if (fills<T, G, 4>(a, grad)) return launch_gp<T, G, 4>(a, grad, st);
-  if (fills<T, G, 2>(a, grad)) return launch_gp<T, G, 2>(a, grad, st);
+  if (a.top_k <= Step<4>::KK && fills_half<T, G, 4>(a, grad))
+    return launch_gp<T, G, 4>(a, grad, st);
+  if (a.top_k <= Step<2>::KK) {
+    const int64_t two = rounds<T, G, 2>(a, grad);
+    if (two < rounds<T, G, 1>(a, grad) && (!grad || a.top_k < Step<2>::KK || two == 1))
+      return launch_gp<T, G, 2>(a, grad, st);
+  }
   return launch_gp<T, G, 1>(a, grad, st);
 }
 
