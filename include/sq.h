@@ -343,8 +343,9 @@ sq_status sq_moe_gather(const void* x, sq_dtype xt, int64_t T, int64_t K,
  *   SQ_BF16); w [T, top_k] fp32, or NULL: 1.  In fp32 from the residual, c
  *   increasing, one fused multiply-add per term (an addition without w), and
  *   rounded once.  Assignments whose pos is outside [0, R) add nothing (their
- *   rows are not read), so a token of none gives residual[t] or 0.  y may be
- *   the residual itself; z must not overlap y.
+ *   rows are not read), so a token of none gives residual[t] or 0.  A row that
+ *   several assignments point to is added for each of them.  y may be the
+ *   residual itself; z must not overlap y.
  */
 sq_status sq_moe_combine(const void* z, sq_dtype t, int64_t R, int64_t N,
                          const int32_t* pos, const float* w, int64_t T,
@@ -361,8 +362,11 @@ sq_status sq_moe_combine(const void* z, sq_dtype t, int64_t R, int64_t N,
  *   dz [R,N] (type t, as dy and z) or NULL, dw [T, top_k] fp32 or NULL; z is
  *   read only for dw (else it may be NULL); w NULL: 1.  dw is summed in fp32
  *   in one fixed order.  Assignments whose pos is outside [0, R) get dw = 0;
- *   rows of dz that no assignment points to keep what they held.  The
- *   residual's gradient is dy.  The arrays must not overlap.
+ *   rows of dz that no assignment points to keep what they held.  For dz no
+ *   two assignments may point to the same row (sq_moe_sort's never do): it
+ *   would hold one of their terms, not the sum, and which one is not defined.
+ *   dw does not need that.  The residual's gradient is dy.  The arrays must
+ *   not overlap.
  */
 sq_status sq_moe_combine_grad(const void* dy, sq_dtype t, int64_t T, int64_t N,
                               const int32_t* pos, const float* w,

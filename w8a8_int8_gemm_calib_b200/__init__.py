@@ -259,7 +259,8 @@ def sq_moe_combine(z, pos, y, weights=None, residual=None, stream=None):
 
 def sq_moe_combine_grad(dy, pos, z=None, weights=None, dz=None, dweights=None, stream=None):
     """Gradients of sq_moe_combine: dz[pos[t, c]] = weights[t, c] * dy[t] and
-    dweights[t, c] = <dy[t], z[pos[t, c]]>, each where its output is given."""
+    dweights[t, c] = <dy[t], z[pos[t, c]]>, each where its output is given.
+    For dz no two assignments may share a row (sq_moe_sort's never do)."""
     T, N = dy.shape
     k = pos.shape[1]
     rows = dz if dz is not None else z
