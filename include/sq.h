@@ -325,7 +325,7 @@ sq_status sq_moe_sort(const void* expert_ids, sq_dtype it, int64_t T,
  *   scale [T] / scale_out [R] fp32: the rows' steps, both or neither.
  *   Assignments whose pos is outside [0, R) are skipped; rows of xs that no
  *   assignment points to keep what they held.  Two assignments must not point
- *   to the same row.
+ *   to the same row, and the arrays must not overlap.
  * Its gradient (of a floating xs) is sq_moe_combine of the rows' gradients
  * without weights.
  */

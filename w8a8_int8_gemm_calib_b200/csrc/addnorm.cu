@@ -18,8 +18,9 @@
 // Bound: HBM.  The call reads 2 and writes 1 value of x's type per element,
 // and writes one code byte (7 bytes for bf16).  Done as an addition and the
 // quantizer, h makes one more trip (9 bytes) and there is one more launch.
-// Measured: 16384 x 8192 bf16 154 us per token (6.1 TB/s) and 170 us with a
-// static step, 2048 x 4096 per token 14 us, 1 x 4096 2.4 us.
+// Measured at 1965 MHz: 16384 x 8192 bf16 157 us per token (6.0 TB/s) and 171
+// us with a static step, 2048 x 4096 per token 15 us, 1 x 4096 2.7 us; wider
+// rows read h and gamma twice from L2: 4096 x 16384 per token 133 us (3.5 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -11,9 +11,12 @@
 // anywhere, so what counts is bytes in flight: a thread has eight 16-byte
 // loads outstanding, of one token's rows or, with few rows a token, of
 // several tokens', and the places of the next step are loaded before the
-// rows of this one.  Measured (bf16 rows of 4096): 16384 tokens of 8 rows, with
-// a residual, 200 us (6.7 TB/s), of 2 rows 86 us; the gradients of 8192 tokens
-// of 8 rows 200 us (5.7 TB/s, half of it writes).
+// rows of this one.  Measured (bf16 rows of 4096, 1965 MHz): 16384 tokens of 8
+// rows, with a residual, 199 us (6.7 TB/s; rows in a random order 205), of 2
+// rows 86 us; the gradients of 8192 tokens of 8 rows 200 us (5.7 TB/s, half of
+// it writes).  So many loads in flight need the clock and the L1: at the 1.1 to
+// 1.7 GHz that a power-capped GEMM leaves behind the first takes 220 to 290 us,
+// and 236 us right behind a kernel that took all of the SMs' shared memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -24,11 +24,13 @@
 // The accumulator has channels along the TMEM lanes and rows along its
 // columns; the epilogue turns it round through shared memory.
 //
-// Measured (bf16 out): 8 experts of 14336x4096 with 1024 rows each 297 us, 3240
-// TOPS, the tensor pipe active 96 % of the time; 64 experts of 4096x4096 with 8
-// rows each 165 us, 6.5 TB/s.  In between the tiles are bound by what an SM
-// takes from L2: 64 such experts with 256 rows each (uneven: tiles of 160 to
-// 256) take 263 us, 2090 TOPS and 4.8 TB/s.
+// Measured (bf16 out): 8 experts of 14336x4096 with 1024 rows each 320 us, 3000
+// TOPS, the tensor pipe active 96 % of the time (power-capped: 1.5 GHz); 64
+// experts of 4096x4096 with 8 rows each 165 us, 6.5 TB/s.  In between neither
+// bound is reached: 64 such experts with 256 rows each take 234 us, 2350 TOPS
+// and 5.4 TB/s, with uneven ones 263 to 280 us; what holds them is not known.
+// With K = 512 the epilogue does: 64 experts of 2048x512 with 512 rows each
+// take 63 us, 33 without it and 48 without its proxy fences alone.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -517,10 +519,14 @@ int band_tiles(int64_t K) {
 }
 
 // Tiles of 32 rows leave room for 11 stages of weights where 256 rows leave
-// 6, and with few rows the stream of the weights is all there is: with 256 and
-// 32 rows, 8 experts of 4096x4096 with a row each take 25.7 and 24.8 us, of
-// 256x4096 10.7 and 9.9, of 14336x4096 with 32 rows each 82.0 and 78.4.  An
-// expert with more rows reads its weights again from L2.
+// 6, and with few rows the stream of the weights is all there is.  us with
+// tiles of 256 / 32 rows: 8 experts of 4096x4096 with a row each 26.0 / 24.8,
+// of 14336x4096 with 32 rows each 81.5 / 75.5; 64 of 4096x4096 with 8 rows each
+// 166.6 / 165.3, with 32 rows each 170.0 / 170.4.  The host knows only the
+// average: an expert with more rows reads its weights from L2 once per 32 of
+// them (those 64 with half of the 2048 rows in one 176.7 / 201.2, with all
+// 28.1 / 82.4), and with short K there are more epilogues (64 of 2048x512 with
+// 32 rows each 23.2 / 25.6).
 int tile_rows(int64_t R, int64_t E) { return R <= 32 * E ? 32 : 256; }
 
 // The number of pairs that can be resident at once is queried once per
